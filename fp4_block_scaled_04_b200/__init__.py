@@ -16,6 +16,7 @@ Formats and layouts (see the header for the arithmetic):
   MXFP6  FP6 (E2M3 or E3M2) codes, four per three bytes + E8M0 scale per 32
   GEMM   C = s_a s_b (A B^T) from NVFP4 operands on the tensor cores
   IF6    per-block FP6 E2M3 / INT6 choice, six-bit codes, flag in bit 7 of the scale
+  MXFP8  FP8 E4M3 codes + E8M0 scale per 32 values (also straight out of the RMS norm)
 """
 from __future__ import annotations
 
@@ -36,14 +37,15 @@ __all__ = [
     "fp4q_quantize_backward", "fp4q_quantize_mxfp6", "FMT_MXFP6_E2M3", "FMT_MXFP6_E3M2",
     "FP6_E2M3", "FP6_E3M2", "fp4q_gemm_nvfp4", "fp4q_gemm_mxfp4", "fp4q_quantize_if6", "FMT_IF6",
     "fp4q_gemm_if4_nvfp4", "fp4q_quantize_if3", "FMT_IF3",
+    "FMT_MXFP8", "fp4q_quantize_mxfp8", "fp4q_rmsnorm_mxfp8", "fp4q_rmsnorm_backward",
 ]
 
 ROWWISE, COLWISE = 1, 2
 RNE, SR = 0, 1
 SCALE_LINEAR, SCALE_SWIZZLED = 0, 1
 E8M0_RNE, E8M0_CEIL, E8M0_OCP_FLOOR = 0, 1, 2
-FMT_NVFP4, FMT_MXFP4, FMT_IF4, FMT_MXFP6_E2M3, FMT_MXFP6_E3M2, FMT_IF6, FMT_IF3 = (
-    0, 1, 2, 3, 4, 5, 6)
+FMT_NVFP4, FMT_MXFP4, FMT_IF4, FMT_MXFP6_E2M3, FMT_MXFP6_E3M2, FMT_IF6, FMT_IF3, FMT_MXFP8 = (
+    0, 1, 2, 3, 4, 5, 6, 7)
 FP6_E2M3, FP6_E3M2 = 0, 1
 _BF16, _FP32 = 0, 1
 
@@ -69,6 +71,7 @@ _lock = threading.Lock()
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
+_F = ctypes.c_float
 _U = ctypes.c_uint
 _U64 = ctypes.c_uint64
 _SZ = ctypes.c_size_t
@@ -106,6 +109,12 @@ _SIGNATURES = {
                                  _P, _P]),
     "fp4q_quantize_if6": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _I, _P, _SZ, _P]),
     "fp4q_quantize_if3": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "fp4q_quantize_mxfp8": (_I, [_P, _I, _I64, _I64, _I64, _I, _P, _P, _I, _P]),
+    "fp4q_rmsnorm_mxfp8": (_I, [_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I, _F, _I, _P, _P, _I,
+                                _P, _P, _P, _P]),
+    "fp4q_rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "fp4q_rmsnorm_backward": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P, _I64, _I64, _I64, _P,
+                                   _P, _P, _SZ, _P]),
 }
 
 
@@ -280,6 +289,120 @@ def fp4q_quantize_mxfp6(x: torch.Tensor, fp6_format: int = FP6_E2M3, e8m0_mode: 
     _check("fp4q_quantize_mxfp6", lib().fp4q_quantize_mxfp6(
         _ptr(x), _dtype(x), rows, cols, ld, fp6_format, e8m0_mode, _ptr(out["q"]),
         _ptr(out["sf"]), scale_layout, _stream(dev)))
+    return out
+
+
+def fp4q_quantize_mxfp8(x: torch.Tensor, e8m0_mode: int = E8M0_CEIL,
+                        scale_layout: int = SCALE_LINEAR, out: dict | None = None) -> dict:
+    """MXFP8 1x32 row-wise; returns {'q': [rows, cols] E4M3 codes, 'sf'}.  Any
+    shape with cols % 32 == 0 may be swizzled (the padding is written as 0)."""
+    rows, cols, ld = _matrix(x)
+    dev = x.device
+    if out is None:
+        out = {"q": _u8((rows, cols), dev),
+               "sf": _u8(fp4q_scale_bytes(rows, cols, 32, scale_layout), dev)}
+    else:
+        _check_mxfp8_out(out, rows, cols, scale_layout, dev)
+    _check("fp4q_quantize_mxfp8", lib().fp4q_quantize_mxfp8(
+        _ptr(x), _dtype(x), rows, cols, ld, e8m0_mode, _ptr(out["q"]), _ptr(out["sf"]),
+        scale_layout, _stream(dev)))
+    return out
+
+
+def _expect(t: torch.Tensor | None, name: str, shape: tuple, dtypes, device) -> None:
+    """A dense tensor of this shape, one of these dtypes, on this device (None passes)."""
+    if t is None:
+        return
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got "
+                         f"shape {tuple(t.shape)}, strides {t.stride()}")
+
+
+def _expect_bytes(t: torch.Tensor, name: str, n: int, device) -> None:
+    """A dense uint8 buffer of at least n bytes on this device."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {n} bytes")
+
+
+def _check_mxfp8_out(out: dict, rows: int, cols: int, scale_layout: int, device) -> None:
+    _expect(out["q"], "out['q']", (rows, cols), (torch.uint8,), device)
+    _expect_bytes(out["sf"], "out['sf']", fp4q_scale_bytes(rows, cols, 32, scale_layout), device)
+
+
+def _like(t: torch.Tensor | None, x: torch.Tensor, name: str) -> int:
+    """Leading dimension of a matrix that has x's shape, dtype and device (0 for None)."""
+    if t is None:
+        return 0
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+        raise ValueError(f"{name} must have the shape {tuple(x.shape)}, dtype {x.dtype} and "
+                         f"device {x.device} of x")
+    return _matrix(t, name)[2]
+
+
+def fp4q_rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                       residual: torch.Tensor | None = None, e8m0_mode: int = E8M0_CEIL,
+                       scale_layout: int = SCALE_LINEAR, want_y: bool = False,
+                       out: dict | None = None) -> dict:
+    """RMS norm of s = x + residual (or x) in MXFP8; returns {'q', 'sf', 'rstd'
+    [rows] FP32, 'sum' (with a residual: s in x's dtype), 'y' (with want_y: the
+    normed values in x's dtype)}.  out['sum'] may be x or residual itself."""
+    rows, cols, ld = _matrix(x)
+    ld_res = _like(residual, x, "residual")
+    dev = x.device
+    _expect(weight, "weight", (cols,), (torch.bfloat16, torch.float32), dev)
+    if out is None:
+        out = {"q": _u8((rows, cols), dev),
+               "sf": _u8(fp4q_scale_bytes(rows, cols, 32, scale_layout), dev),
+               "rstd": torch.empty(rows, dtype=torch.float32, device=dev)}
+        if residual is not None:
+            out["sum"] = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        if want_y:
+            out["y"] = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+    else:
+        _check_mxfp8_out(out, rows, cols, scale_layout, dev)
+        _expect(out.get("rstd"), "out['rstd']", (rows,), (torch.float32,), dev)
+        _expect(out.get("sum"), "out['sum']", (rows, cols), (x.dtype,), dev)
+        _expect(out.get("y"), "out['y']", (rows, cols), (x.dtype,), dev)
+    _check("fp4q_rmsnorm_mxfp8", lib().fp4q_rmsnorm_mxfp8(
+        _ptr(x), _dtype(x), rows, cols, ld, _ptr(residual), ld_res, _ptr(weight), _dtype(weight),
+        eps, e8m0_mode, _ptr(out["q"]), _ptr(out["sf"]), scale_layout, _ptr(out.get("rstd")),
+        _ptr(out.get("sum")), _ptr(out.get("y")), _stream(dev)))
+    return out
+
+
+def fp4q_rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                          rstd: torch.Tensor, dsum: torch.Tensor | None = None,
+                          out: dict | None = None,
+                          workspace: torch.Tensor | None = None) -> dict:
+    """Gradients of the norm: {'dx': [rows, cols] in x's dtype (of x and of the
+    residual alike), 'dweight': [cols] FP32}.  x is the forward pass's sum (x
+    itself without a residual), dsum the gradient along the residual stream."""
+    rows, cols, ld = _matrix(x)
+    ld_dy, ld_dsum = _like(dy, x, "dy"), _like(dsum, x, "dsum")
+    dev = x.device
+    _expect(weight, "weight", (cols,), (torch.bfloat16, torch.float32), dev)
+    _expect(rstd, "rstd", (rows,), (torch.float32,), dev)
+    if out is None:
+        out = {"dx": torch.empty((rows, cols), dtype=x.dtype, device=dev),
+               "dweight": torch.empty(cols, dtype=torch.float32, device=dev)}
+    else:
+        _expect(out["dx"], "out['dx']", (rows, cols), (x.dtype,), dev)
+        _expect(out["dweight"], "out['dweight']", (cols,), (torch.float32,), dev)
+    need = int(lib().fp4q_rmsnorm_backward_workspace_bytes(rows, cols))
+    if workspace is None:
+        workspace = _u8(need, dev)
+    else:
+        _expect_bytes(workspace, "workspace", need, dev)
+    _check("fp4q_rmsnorm_backward", lib().fp4q_rmsnorm_backward(
+        _ptr(dy), ld_dy, _ptr(x), ld, _dtype(x), _ptr(weight), _dtype(weight), _ptr(rstd),
+        _ptr(dsum), ld_dsum, rows, cols, _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(workspace),
+        workspace.numel(), _stream(dev)))
     return out
 
 

@@ -725,9 +725,10 @@ fp4q_status fp4q_dequantize(int format, const uint8_t *q, const uint8_t *sf, int
                             int block_rows, int block_cols, const float *tensor_scale,
                             int64_t rows, int64_t cols, void *y, int y_dtype, void *stream) {
   DeviceGuard guard;
-  if (format < FP4Q_FMT_NVFP4 || format > FP4Q_FMT_IF3) return FP4Q_ERR_INVALID_ARG;
+  if (format < FP4Q_FMT_NVFP4 || format > FP4Q_FMT_MXFP8) return FP4Q_ERR_INVALID_ARG;
   const bool fp6 = format == FP4Q_FMT_MXFP6_E2M3 || format == FP4Q_FMT_MXFP6_E3M2;
-  const bool pow2 = fp6 || format == FP4Q_FMT_MXFP4;   // E8M0 scales, no tensor scale
+  const bool mxfp8 = format == FP4Q_FMT_MXFP8;
+  const bool pow2 = fp6 || mxfp8 || format == FP4Q_FMT_MXFP4;   // E8M0 scales, no tensor scale
   if (!valid_layout(scale_layout) || !valid_dtype(y_dtype)) return FP4Q_ERR_INVALID_ARG;
   if (rows < 0 || cols < 0) return FP4Q_ERR_INVALID_ARG;
   const bool shape_ok =
@@ -741,12 +742,15 @@ fp4q_status fp4q_dequantize(int format, const uint8_t *q, const uint8_t *sf, int
   if (!q || !sf || !y) return FP4Q_ERR_INVALID_ARG;
   if (!pow2 && !tensor_scale) return FP4Q_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(y)) return FP4Q_ERR_MISALIGNED;
-  if (block_rows == 1) FP4Q_TRY(check_swizzle(scale_layout, rows, cols / block_cols));
+  // the MXFP8 writers pad the swizzled layout; the others need whole tiles
+  if (block_rows == 1 && !mxfp8) FP4Q_TRY(check_swizzle(scale_layout, rows, cols / block_cols));
   Launch L;
   FP4Q_TRY(bind_device(q, stream, &L));
   FP4Q_TRY(check_dev(sf, false));
   FP4Q_TRY(check_dev(y, false));
   FP4Q_TRY(check_dev(pow2 ? nullptr : tensor_scale, true));
+  if (mxfp8)
+    return cuda_status(launch_mxfp8_dequant(q, sf, scale_layout, rows, cols, y, y_dtype, L));
   if (format == FP4Q_FMT_IF6)
     return cuda_status(
         launch_if6_dequant(q, sf, scale_layout, tensor_scale, rows, cols, y, y_dtype, L));
@@ -759,6 +763,101 @@ fp4q_status fp4q_dequantize(int format, const uint8_t *q, const uint8_t *sf, int
         format == FP4Q_FMT_MXFP6_E2M3 ? FP4Q_FP6_E2M3 : FP4Q_FP6_E3M2, y, y_dtype, L));
   return cuda_status(launch_dequant(format, q, sf, scale_layout, block_rows, block_cols,
                                     tensor_scale, rows, cols, y, y_dtype, L));
+}
+
+fp4q_status fp4q_quantize_mxfp8(const void *x, int dtype, int64_t rows, int64_t cols,
+                                int64_t ld, int e8m0_mode, uint8_t *q, uint8_t *sf,
+                                int scale_layout, void *stream) {
+  DeviceGuard guard;
+  FP4Q_TRY(check_matrix(x, dtype, rows, cols, ld));
+  if (e8m0_mode < FP4Q_E8M0_RNE || e8m0_mode > FP4Q_E8M0_OCP_FLOOR) return FP4Q_ERR_INVALID_ARG;
+  if (!valid_layout(scale_layout)) return FP4Q_ERR_INVALID_ARG;
+  if (cols % 32 != 0) return FP4Q_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0 || cols == 0) return FP4Q_OK;
+  if (!q || !sf) return FP4Q_ERR_INVALID_ARG;
+  if (!aligned16(q)) return FP4Q_ERR_MISALIGNED;
+  Launch L;
+  FP4Q_TRY(bind_device(x, stream, &L));
+  FP4Q_TRY(check_dev(q, false));
+  FP4Q_TRY(check_dev(sf, false));
+  return cuda_status(launch_mxfp8(x, dtype, rows, cols, ld, e8m0_mode, q, sf, scale_layout, L));
+}
+
+fp4q_status fp4q_rmsnorm_mxfp8(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                               const void *residual, int64_t ld_residual, const void *weight,
+                               int weight_dtype, float eps, int e8m0_mode, uint8_t *q,
+                               uint8_t *sf, int scale_layout, float *rstd, void *sum, void *y,
+                               void *stream) {
+  DeviceGuard guard;
+  FP4Q_TRY(check_matrix(x, dtype, rows, cols, ld));
+  if (residual) FP4Q_TRY(check_matrix(residual, dtype, rows, cols, ld_residual));
+  if (!valid_dtype(weight_dtype) || !(eps >= 0.0f)) return FP4Q_ERR_INVALID_ARG;
+  if (e8m0_mode < FP4Q_E8M0_RNE || e8m0_mode > FP4Q_E8M0_OCP_FLOOR) return FP4Q_ERR_INVALID_ARG;
+  if (!valid_layout(scale_layout)) return FP4Q_ERR_INVALID_ARG;
+  if (cols % 32 != 0 || cols > kNormMaxCols) return FP4Q_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0 || cols == 0) return FP4Q_OK;
+  if (!weight || !q || !sf) return FP4Q_ERR_INVALID_ARG;
+  if (!aligned16(weight) || !aligned16(q) || !aligned16(rstd) || !aligned16(sum) || !aligned16(y))
+    return FP4Q_ERR_MISALIGNED;
+  // an in-place sum needs the same place for every element
+  if (sum && ((sum == x && ld != cols) || (sum == residual && ld_residual != cols)))
+    return FP4Q_ERR_INVALID_ARG;
+  Launch L;
+  FP4Q_TRY(bind_device(x, stream, &L));
+  FP4Q_TRY(check_dev(residual, true));
+  FP4Q_TRY(check_dev(weight, false));
+  FP4Q_TRY(check_dev(q, false));
+  FP4Q_TRY(check_dev(sf, false));
+  FP4Q_TRY(check_dev(rstd, true));
+  FP4Q_TRY(check_dev(sum, true));
+  FP4Q_TRY(check_dev(y, true));
+  return cuda_status(launch_rmsnorm(x, dtype, rows, cols, ld, residual, ld_residual, weight,
+                                    weight_dtype, eps, e8m0_mode, q, sf, scale_layout, rstd, sum,
+                                    y, L));
+}
+
+size_t fp4q_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0) return 0;
+  return static_cast<size_t>((rows < kNormParts ? rows : kNormParts) * cols) * sizeof(float);
+}
+
+fp4q_status fp4q_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *x, int64_t ld,
+                                  int dtype, const void *weight, int weight_dtype,
+                                  const float *rstd, const void *dsum, int64_t ld_dsum,
+                                  int64_t rows, int64_t cols, void *dx, float *dweight,
+                                  void *workspace, size_t ws_bytes, void *stream) {
+  DeviceGuard guard;
+  FP4Q_TRY(check_matrix(dy, dtype, rows, cols, ld_dy));
+  FP4Q_TRY(check_matrix(x, dtype, rows, cols, ld));
+  if (dsum) FP4Q_TRY(check_matrix(dsum, dtype, rows, cols, ld_dsum));
+  if (!valid_dtype(weight_dtype)) return FP4Q_ERR_INVALID_ARG;
+  if (cols % 32 != 0 || cols > kNormMaxCols) return FP4Q_ERR_UNSUPPORTED_SHAPE;
+  if (cols == 0) return FP4Q_OK;
+  if (!dweight) return FP4Q_ERR_INVALID_ARG;
+  if (!aligned16(dweight)) return FP4Q_ERR_MISALIGNED;
+  Launch L;
+  if (rows == 0) {
+    FP4Q_TRY(bind_device(dweight, stream, &L));
+    return cuda_status(cudaMemsetAsync(dweight, 0, sizeof(float) * cols, L.stream));
+  }
+  if (!weight || !rstd || !dx) return FP4Q_ERR_INVALID_ARG;
+  if (!workspace || ws_bytes < fp4q_rmsnorm_backward_workspace_bytes(rows, cols))
+    return FP4Q_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(weight) || !aligned16(rstd) || !aligned16(dx) || !aligned16(workspace))
+    return FP4Q_ERR_MISALIGNED;
+  if (dx == x || (dx == dy && ld_dy != cols) || (dx == dsum && ld_dsum != cols))
+    return FP4Q_ERR_INVALID_ARG;
+  FP4Q_TRY(bind_device(dy, stream, &L));
+  FP4Q_TRY(check_dev(x, false));
+  FP4Q_TRY(check_dev(weight, false));
+  FP4Q_TRY(check_dev(rstd, false));
+  FP4Q_TRY(check_dev(dsum, true));
+  FP4Q_TRY(check_dev(dx, false));
+  FP4Q_TRY(check_dev(dweight, false));
+  FP4Q_TRY(check_dev(workspace, false));
+  return cuda_status(launch_rmsnorm_backward(dy, ld_dy, x, ld, dtype, weight, weight_dtype, rstd,
+                                             dsum, ld_dsum, rows, cols, dx, dweight,
+                                             static_cast<float *>(workspace), L));
 }
 
 }  // extern "C"

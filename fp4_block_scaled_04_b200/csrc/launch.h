@@ -132,6 +132,28 @@ cudaError_t launch_mxfp6_dequant(const uint8_t *q, const uint8_t *sf, int scale_
                                  int64_t rows, int64_t cols, int fp6_format, void *y,
                                  int y_dtype, const Launch &L);
 
+// MXFP8: E4M3 codes with E8M0 scales per 32 values, and its decode
+cudaError_t launch_mxfp8(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                         int e8m0_mode, uint8_t *q, uint8_t *sf, int scale_layout,
+                         const Launch &L);
+cudaError_t launch_mxfp8_dequant(const uint8_t *q, const uint8_t *sf, int scale_layout,
+                                 int64_t rows, int64_t cols, void *y, int y_dtype,
+                                 const Launch &L);
+
+// RMSNorm (+ residual) with MXFP8 output, and its backward pass: at most
+// kNormParts row parts of dweight, [parts][cols] floats in `part`
+constexpr int64_t kNormMaxCols = 32768;
+constexpr int64_t kNormParts = 592;
+cudaError_t launch_rmsnorm(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                           const void *res, int64_t ld_res, const void *weight, int weight_dtype,
+                           float eps, int e8m0_mode, uint8_t *q, uint8_t *sf, int scale_layout,
+                           float *rstd, void *sum, void *y, const Launch &L);
+cudaError_t launch_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *s, int64_t ld_s,
+                                    int dtype, const void *weight, int weight_dtype,
+                                    const float *rstd, const void *dsum, int64_t ld_dsum,
+                                    int64_t rows, int64_t cols, void *dx, float *dweight,
+                                    float *part, const Launch &L);
+
 // Options of the tensor-core GEMM: the product is scaled by a = RN(RN(s_a s_b)
 // * alpha_mul); with a second accumulator (the IF4 GEMM) that one is scaled by
 // RN(a * alpha_int); withhold != 0 (a failure-detection test hook) issues no

@@ -87,7 +87,8 @@ typedef enum {
   FP4Q_FMT_MXFP6_E2M3 = 3,   /* codes packed four per three bytes */
   FP4Q_FMT_MXFP6_E3M2 = 4,
   FP4Q_FMT_IF6 = 5,          /* 6-bit codes, four per three bytes */
-  FP4Q_FMT_IF3 = 6           /* 3-bit codes, eight per three bytes */
+  FP4Q_FMT_IF3 = 6,          /* 3-bit codes, eight per three bytes */
+  FP4Q_FMT_MXFP8 = 7         /* E4M3 codes, one per byte */
 } fp4q_format;
 typedef enum { FP4Q_FP6_E2M3 = 0, FP4Q_FP6_E3M2 = 1 } fp4q_fp6_format;
 
@@ -343,6 +344,72 @@ fp4q_status fp4q_quantize_if3(const void *x, int dtype, int64_t rows, int64_t co
 fp4q_status fp4q_quantize_mxfp6(const void *x, int dtype, int64_t rows, int64_t cols,
                                 int64_t ld, int fp6_format, int e8m0_mode, uint8_t *q,
                                 uint8_t *sf, int scale_layout, void *stream);
+
+/* MXFP8 1x32, row-wise: OCP FP8 E4M3 elements (largest 448, no infinity) with
+ * E8M0 block scales -- the 8-bit activation that the block-scaled tensor core
+ * multiplies with MXFP4 weights (fp4q_gemm_mxfp8_mxfp4).  The exponent e as in
+ * fp4q_quantize_mxfp6 with qmax = 448 = 1.75 * 2^8:
+ *   FP4Q_E8M0_CEIL       smallest power of two >= RN(m / 448): no element
+ *                        saturates (the binding's default)
+ *   FP4Q_E8M0_RNE        RN(m / 448) to the nearest power of two
+ *   FP4Q_E8M0_OCP_FLOOR  2^(floor(log2 m) - 8)
+ * Elements v = RN(x * 2^-e), E4M3 round to nearest even with saturation; a
+ * block of zeros has e = -127.
+ *   q    [rows, cols] E4M3 codes, 16-byte aligned
+ *   sf   biased exponents e + 127 in scale_layout.  Any number of rows and
+ *        blocks may be swizzled here: the layout's rows are rounded up to 128
+ *        and its columns up to 4 (fp4q_scale_bytes(rows, cols, 32, layout)
+ *        bytes), and the padding bytes are written as 0
+ * Shape: cols % 32 == 0.  fp4q_dequantize(FP4Q_FMT_MXFP8, ..., 1, 32, NULL, ...)
+ * decodes it, y = RN(code * 2^e), from either layout at any number of rows. */
+fp4q_status fp4q_quantize_mxfp8(const void *x, int dtype, int64_t rows, int64_t cols,
+                                int64_t ld, int e8m0_mode, uint8_t *q, uint8_t *sf,
+                                int scale_layout, void *stream);
+
+/* Root-mean-square norm with the residual's addition and an MXFP8 output: the
+ * producer of the activation in front of a block-scaled product.  Per row of H
+ * = cols values, in FP32:
+ *   s    = RN_T(x + residual), or x without a residual (T the dtype of x)
+ *   rstd = 1 / sqrt(mean(s^2) + eps)          (the mean in the kernel's order)
+ *   y    = RN(RN(s * rstd) * weight)
+ *   q, sf  MXFP8 of y, as fp4q_quantize_mxfp8 (y itself is not rounded first)
+ *   x, residual  [rows, cols] of dtype, leading dimensions ld, ld_residual;
+ *                residual may be NULL
+ *   weight       [cols] of weight_dtype
+ *   rstd         [rows] floats, or NULL
+ *   sum          [rows, cols] of dtype <- s, or NULL; it may be x or residual
+ *                itself when that is dense (leading dimension cols)
+ *   y            [rows, cols] of dtype <- RN_T(y), or NULL (for a router)
+ *   eps          >= 0
+ * Shape: cols % 32 == 0, cols <= 32768.  All pointers 16-byte aligned. */
+fp4q_status fp4q_rmsnorm_mxfp8(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld,
+                               const void *residual, int64_t ld_residual, const void *weight,
+                               int weight_dtype, float eps, int e8m0_mode, uint8_t *q,
+                               uint8_t *sf, int scale_layout, float *rstd, void *sum, void *y,
+                               void *stream);
+
+/* Backward pass of the norm (the quantization passes its gradient straight
+ * through).  With g = dy the gradient of y and s, rstd from the forward pass:
+ *   dx      = RN_T(rstd * (weight g - s rstd^2 mean(weight g s)) + dsum)
+ *             (the gradient of x and of the residual alike)
+ *   dweight = sum over rows of g * s * rstd, FP32
+ *   dy, x, dsum  [rows, cols] of dtype, leading dimensions ld_dy, ld,
+ *                ld_dsum; x is the forward pass's s.  dsum, the gradient that
+ *                reaches s along the residual stream, may be NULL
+ *   dx           [rows, cols] of dtype, dense; may be dy or dsum itself when
+ *                that is dense
+ *   dweight      [cols] floats, overwritten (zeros when rows == 0)
+ *   workspace    >= fp4q_rmsnorm_backward_workspace_bytes(rows, cols) bytes
+ *                when rows > 0; the calls that overlap on the GPU need one each
+ * The sums' order depends on the shape, the types and the GPU's number of SMs
+ * alone: equal calls give equal bits.
+ * Shape: cols % 32 == 0, cols <= 32768.  All pointers 16-byte aligned. */
+size_t fp4q_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+fp4q_status fp4q_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *x, int64_t ld,
+                                  int dtype, const void *weight, int weight_dtype,
+                                  const float *rstd, const void *dsum, int64_t ld_dsum,
+                                  int64_t rows, int64_t cols, void *dx, float *dweight,
+                                  void *workspace, size_t ws_bytes, void *stream);
 
 /* Block-scaled NVFP4 GEMM on the tensor cores: the consumer of the
  * quantized operands.  Qiita note on NVFP4 training ("Blockwise", "誤差逆伝播と
