@@ -38,6 +38,7 @@ __all__ = [
     "FP6_E2M3", "FP6_E3M2", "fp4q_gemm_nvfp4", "fp4q_gemm_mxfp4", "fp4q_quantize_if6", "FMT_IF6",
     "fp4q_gemm_if4_nvfp4", "fp4q_quantize_if3", "FMT_IF3",
     "FMT_MXFP8", "fp4q_quantize_mxfp8", "fp4q_rmsnorm_mxfp8", "fp4q_rmsnorm_backward",
+    "fp4q_gemm_mxfp8_mxfp4",
 ]
 
 ROWWISE, COLWISE = 1, 2
@@ -115,6 +116,7 @@ _SIGNATURES = {
     "fp4q_rmsnorm_backward_workspace_bytes": (_SZ, [_I64, _I64]),
     "fp4q_rmsnorm_backward": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P, _I64, _I64, _I64, _P,
                                    _P, _P, _SZ, _P]),
+    "fp4q_gemm_mxfp8_mxfp4": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _I64, _P, _P]),
 }
 
 
@@ -470,6 +472,48 @@ def fp4q_gemm_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor, sfb: 
     _check("fp4q_gemm_mxfp4", lib().fp4q_gemm_mxfp4(
         _ptr(qa), _ptr(sfa), _ptr(qb), _ptr(sfb), M, N, K, _ptr(c), cdt,
         c.stride(0) if M > 1 else N, _ptr(status), _stream(qa.device)))
+    return c
+
+
+def _matrix_out(out: torch.Tensor | None, rows: int, cols: int, dtype: torch.dtype, device
+                ) -> tuple[torch.Tensor, int, int]:
+    """The output matrix (a new one, or the caller's [rows, cols] with unit column
+    stride), its dtype code and its leading dimension."""
+    if out is None:
+        out = torch.empty((rows, cols), dtype=dtype, device=device)
+    elif out.device != device or tuple(out.shape) != (rows, cols):
+        raise ValueError(f"out must be a [{rows}, {cols}] tensor on {device}")
+    return out, _dtype(out), _matrix(out, "out")[2]
+
+
+def _status_ptr(status: torch.Tensor | None, device):
+    if status is not None and (status.dtype != torch.int32 or status.device != device):
+        raise ValueError(f"status must be an int32 tensor on {device}")
+    return _ptr(status)
+
+
+def fp4q_gemm_mxfp8_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor,
+                          sfb: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+                          out: torch.Tensor | None = None,
+                          status: torch.Tensor | None = None) -> torch.Tensor:
+    """C [M, N] = A B^T from MXFP8 tokens (codes qa [M, K], any M) and MXFP4
+    weights (codes qb [N, K/2]), both with swizzled 1x32 scales (as
+    fp4q_quantize_mxfp8 / fp4q_rmsnorm_mxfp8 and fp4q_quantize_mxfp4 write them)."""
+    if not qa.is_cuda:
+        raise ValueError("qa must be a CUDA tensor")
+    if qa.dim() != 2 or qb.dim() != 2 or qa.shape[1] != 2 * qb.shape[1]:
+        raise ValueError("qa must be [M, K] and qb [N, K/2], got "
+                         f"{tuple(qa.shape)} and {tuple(qb.shape)}")
+    (M, K), N, dev = qa.shape, qb.shape[0], qa.device
+    _expect(qa, "qa", (M, K), (torch.uint8,), dev)
+    _expect(qb, "qb", (N, K // 2), (torch.uint8,), dev)
+    if K % 32 == 0:
+        _expect_bytes(sfa, "sfa", fp4q_scale_bytes(M, K, 32, SCALE_SWIZZLED), dev)
+        _expect_bytes(sfb, "sfb", fp4q_scale_bytes(N, K, 32, SCALE_SWIZZLED), dev)
+    c, cdt, ldc = _matrix_out(out, M, N, out_dtype, dev)
+    _check("fp4q_gemm_mxfp8_mxfp4", lib().fp4q_gemm_mxfp8_mxfp4(
+        _ptr(qa), _ptr(sfa), _ptr(qb), _ptr(sfb), M, N, K, _ptr(c), cdt, ldc,
+        _status_ptr(status, dev), _stream(dev)))
     return c
 
 

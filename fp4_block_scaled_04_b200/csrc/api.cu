@@ -18,6 +18,7 @@ constexpr size_t kWorkspaceBytes = 256;  // one float amax, padded
 int g_num_sms[64];
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 int elem_size(int dtype) { return dtype == FP4Q_BF16 ? 2 : 4; }
 
@@ -858,6 +859,41 @@ fp4q_status fp4q_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *x, 
   return cuda_status(launch_rmsnorm_backward(dy, ld_dy, x, ld, dtype, weight, weight_dtype, rstd,
                                              dsum, ld_dsum, rows, cols, dx, dweight,
                                              static_cast<float *>(workspace), L));
+}
+
+fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
+                                  const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
+                                  int c_dtype, int64_t ldc, int *status, void *stream) {
+  DeviceGuard guard;
+  if (!valid_dtype(c_dtype)) return FP4Q_ERR_INVALID_ARG;
+  if (M < 0 || N < 0 || K < 0 || ldc < N) return FP4Q_ERR_INVALID_ARG;
+  if (N % 128 != 0 || K % 128 != 0) return FP4Q_ERR_UNSUPPORTED_SHAPE;
+  // tile counts and coordinates are 32-bit
+  constexpr int64_t kMost = int64_t{1} << 30;
+  if (M > kMost || N > kMost || K > kMost || (M > 0 && N > (int64_t{1} << 40) / M))
+    return FP4Q_ERR_UNSUPPORTED_SHAPE;
+  if (M == 0 || N == 0) return FP4Q_OK;
+  if (!c) return FP4Q_ERR_INVALID_ARG;
+  const int64_t esz = elem_size(c_dtype);
+  if (!aligned16(c) || (ldc * esz) % 16 != 0) return FP4Q_ERR_MISALIGNED;
+  if (K > 0) {
+    if (!qa || !sfa || !qb || !sfb) return FP4Q_ERR_INVALID_ARG;
+    if (!aligned16(qa) || !aligned16(sfa) || !aligned32(qb) || !aligned16(sfb))
+      return FP4Q_ERR_MISALIGNED;
+  }
+  Launch L;
+  FP4Q_TRY(bind_device(c, stream, &L));
+  if (K == 0)   // an empty sum
+    return cuda_status(cudaMemset2DAsync(c, static_cast<size_t>(ldc * esz), 0,
+                                         static_cast<size_t>(N * esz), static_cast<size_t>(M),
+                                         L.stream));
+  FP4Q_TRY(check_dev(qa, false));
+  FP4Q_TRY(check_dev(sfa, false));
+  FP4Q_TRY(check_dev(qb, false));
+  FP4Q_TRY(check_dev(sfb, false));
+  FP4Q_TRY(check_dev(status, true));
+  return cuda_status(
+      launch_gemm_mxfp8_mxfp4(qa, sfa, qb, sfb, M, N, K, c, c_dtype, ldc, status, L));
 }
 
 }  // extern "C"

@@ -177,6 +177,12 @@ cudaError_t launch_gemm_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8
                               const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
                               int c_dtype, int64_t ldc, int *status, const Launch &L);
 
+// C[M, N] = A B^T from MXFP8 tokens (any M) and MXFP4 weights, both with E8M0
+// scales per 32 values in the 128x4 tile layout, on the tensor cores
+cudaError_t launch_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
+                                    const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
+                                    int c_dtype, int64_t ldc, int *status, const Launch &L);
+
 // IF4 x NVFP4 in one pass over the split operands: C = RN(RN(acc_fp * a) +
 // RN(acc_int * RN(a * RN(6/7)))), acc_int accumulating both INT4 parts; FP32
 // output, N % 128 == 0

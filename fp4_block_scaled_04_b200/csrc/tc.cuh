@@ -1,0 +1,223 @@
+// tc.cuh -- the tensor-core plumbing shared by the GEMM kernels: mbarriers
+// with bounded waits, TMA loads, tcgen05 copies, commits and tensor-memory
+// reads, matrix descriptors, and the tensor-map encoder.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+
+namespace fp4q {
+
+constexpr long long kWaitCycles = 2000000000LL;  // ~1 s at the B200's clock
+
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Shared-memory matrix descriptor, K-major with 128-byte swizzle: rows of
+// 128 bytes, 8-row groups 1024 bytes apart (SBO), LBO 1 (unused for this
+// layout), descriptor version 1, layout type 2.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t{1} << 16) |
+         (uint64_t{1024 >> 4} << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+
+// Descriptor of one 512-byte scale tile for the 32x128b copy: 32 rows of 16
+// bytes, no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t desc_sf(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (uint64_t{128 >> 4} << 32) |
+         (uint64_t{1} << 46);
+}
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// true once the phase with this parity has completed; false after about a
+// second without completion
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity))
+    if (clock64() - t0 > kWaitCycles) return false;
+  return true;
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   bar)
+               : "memory");
+}
+__device__ __forceinline__ void tc_copy_sf(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+// 16 consecutive FP32 accumulator columns of this thread's row (warp w reads
+// lanes 32 (w % 4) .. + 31); the wait is separate so that loads can overlap
+__device__ __forceinline__ void tc_load16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+
+// TMA tile load of a 2-D box (x in bytes along the row, y rows), completing
+// on an mbarrier; no multicast
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// contiguous bulk copy (16-byte aligned, size a multiple of 16) completing
+// on an mbarrier; no multicast
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// One block-scaled MMA of 32 values of K, 8-bit containers: A (the operand in
+// the 128 lanes) MXFP4, its E2M1 codes 16 to a 16-byte chunk of shared memory
+// (8 bytes of codes, 8 of padding), B MXFP8 E4M3 bytes; one E8M0 scale per row
+// and 32 values, its byte within the 32-bit tensor-memory cell named by idesc.
+__device__ __forceinline__ void tc_mma_mx4x8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+
+// Its instruction descriptor for M = 128 and N columns: A E2M1 (format 5 in
+// bits 7-9), B E4M3 (format 0 in bits 10-12), N / 8 in bits 17-22, E8M0 scales
+// (bit 23), M / 16 from bit 24; `byte` (0..3) is the scale byte of this K step
+// for A (bits 29-30) and B (bits 4-5).
+__device__ __forceinline__ constexpr uint32_t idesc_mx4x8(uint32_t n, uint32_t byte) {
+  return (5u << 7) | ((n >> 3) << 17) | (1u << 23) | (8u << 24) | (byte << 29) | (byte << 4);
+}
+
+// The MMAs of one K-tile of 128 values: the scale tiles of A (128 rows) and B
+// (NSFB tiles of 128 columns) into tensor memory at sfa and sfb, four MMAs.
+template <int NSFB>
+__device__ __forceinline__ void mma_ktile_mx4x8(uint32_t d, uint32_t a_smem, uint32_t b_smem,
+                                                uint32_t sfa_smem, uint32_t sfb_smem,
+                                                uint32_t sfa, uint32_t sfb, uint32_t n,
+                                                bool accumulate) {
+  tc_copy_sf(sfa, desc_sf(sfa_smem));
+#pragma unroll
+  for (int h = 0; h < NSFB; ++h) tc_copy_sf(sfb + 4u * h, desc_sf(sfb_smem + 512u * h));
+  const uint64_t da = desc_sw128(a_smem), db = desc_sw128(b_smem);
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k)                       // 32 values = 32 bytes = 2 units
+    tc_mma_mx4x8(d, da + 2u * k, db + 2u * k, idesc_mx4x8(n, k), sfa | (k << 30), sfb | (k << 30),
+                 accumulate || k != 0);
+}
+
+// Cluster barrier (every thread of every CTA of the cluster arrives) and
+// shared memory of a peer CTA.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_load(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// cuTensorMapEncodeTiled, reached through the runtime (no link to the driver
+// library)
+inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    cudaGetLastError();
+  });
+  return fn;
+}
+
+// An MXFP4 weight matrix [rows, K] (packed E2M1 codes, rows of K / 2 bytes) read
+// as boxes of 128 values x 128 rows: TMA spreads the codes into the 8-bit
+// containers of the mixed MMA, 128-byte swizzle.  K % 128 == 0, base 32-byte
+// aligned; rows past the matrix read as 0.
+inline bool make_map_mxfp4(CUtensorMap *map, const uint8_t *base, int64_t rows, int64_t K) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t box[2] = {128, 128}, estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<uint8_t *>(base), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// A byte matrix [rows, K] (E4M3 codes) read as boxes of 128 bytes x box_rows
+// rows, 128-byte swizzle; rows past the matrix read as 0.
+inline bool make_map_mxfp8(CUtensorMap *map, const uint8_t *base, int64_t rows, int64_t K,
+                           int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K)};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+}  // namespace fp4q

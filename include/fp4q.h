@@ -561,6 +561,27 @@ fp4q_status fp4q_quantize_nvfp4_noalloc(const void *x, int dtype, int64_t rows, 
                                         uint8_t *q_row, uint8_t *sf_row, uint8_t *q_col,
                                         uint8_t *sf_col, int scale_layout, void *stream);
 
+/* MXFP8 x MXFP4 on the tensor cores, for any number of tokens: the product
+ * behind fp4q_rmsnorm_mxfp8 / fp4q_quantize_mxfp8 with weights quantized by
+ * fp4q_quantize_mxfp4.
+ *   C[m, n] = RN(sum_k A[m, k] B[n, k]),  A = codes * 2^e (E4M3, 1x32),
+ *   B = codes * 2^e (E2M1, 1x32), accumulated in FP32 by tcgen05.mma
+ *   kind::mxf8f6f4 (the order of the additions is the hardware's and the
+ *   split's; equal calls on one GPU give equal bits).
+ *   qa, sfa   A codes [M, K] and scales, FP4Q_SCALE_SWIZZLED_128x4 (rows padded
+ *             to 128 as fp4q_quantize_mxfp8 writes them)
+ *   qb, sfb   B codes [N, K/2] and scales, FP4Q_SCALE_SWIZZLED_128x4
+ *   c, c_dtype, ldc  output [M, ldc] row-major, FP32 or BF16 (RNE of the FP32
+ *             value); ldc >= N
+ *   status    device int or NULL: set to 1 if a wait inside the kernel ran out
+ *             (about a second; results are then not valid).  Never cleared
+ * Shape: M >= 0, N % 128 == 0, K % 128 == 0; K == 0 writes zeros.  qb 32-byte
+ * aligned, the other pointers 16; ldc * element size % 16 == 0.  Nothing is
+ * allocated. */
+fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
+                                  const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
+                                  int c_dtype, int64_t ldc, int *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -76,3 +76,18 @@ def test_norm_backward(L):
         assert backward(L, **{k: ODD}) == ALIGN
     assert backward(L, dx=A2) == ARG                   # dx may not be x
     assert backward(L, ld_dy=128) == ARG               # in place, but not at the same places
+
+
+def gemm(L, qa=A, sfa=A, qb=A, sfb=A, M=3, N=128, K=256, c=A, dtype=0, ldc=128, status=None):
+    return L.fp4q_gemm_mxfp8_mxfp4(qa, sfa, qb, sfb, M, N, K, c, dtype, ldc, status, None)
+
+
+def test_gemm(L):
+    assert gemm(L, dtype=2) == ARG and gemm(L, ldc=120) == ARG and gemm(L, M=-1) == ARG
+    for k in ("qa", "sfa", "qb", "sfb", "c"):
+        assert gemm(L, **{k: None}) == ARG and gemm(L, **{k: ODD}) == ALIGN
+    assert gemm(L, qb=ctypes.c_void_p(0x7F0000000010)) == ALIGN     # 32 bytes for the weights
+    assert gemm(L, N=64, ldc=64) == SHAPE and gemm(L, K=160) == SHAPE
+    assert gemm(L, M=1 << 20, N=1 << 29, ldc=1 << 29) == SHAPE
+    assert gemm(L, ldc=129) == ALIGN
+    assert gemm(L, M=0, qa=None, c=None) == OK and gemm(L, N=0, ldc=0) == OK
