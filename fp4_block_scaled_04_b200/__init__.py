@@ -38,7 +38,7 @@ __all__ = [
     "FP6_E2M3", "FP6_E3M2", "fp4q_gemm_nvfp4", "fp4q_gemm_mxfp4", "fp4q_quantize_if6", "FMT_IF6",
     "fp4q_gemm_if4_nvfp4", "fp4q_quantize_if3", "FMT_IF3",
     "FMT_MXFP8", "fp4q_quantize_mxfp8", "fp4q_rmsnorm_mxfp8", "fp4q_rmsnorm_backward",
-    "fp4q_gemm_mxfp8_mxfp4",
+    "fp4q_gemm_mxfp8_mxfp4", "fp4q_moe_mxfp4",
 ]
 
 ROWWISE, COLWISE = 1, 2
@@ -117,6 +117,9 @@ _SIGNATURES = {
     "fp4q_rmsnorm_backward": (_I, [_P, _I64, _P, _I64, _I, _P, _I, _P, _P, _I64, _I64, _I64, _P,
                                    _P, _P, _SZ, _P]),
     "fp4q_gemm_mxfp8_mxfp4": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _I64, _P, _P]),
+    "fp4q_moe_mxfp4_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "fp4q_moe_mxfp4": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I, _P,
+                            _I, _I64, _P, _SZ, _P, _P]),
 }
 
 
@@ -514,6 +517,40 @@ def fp4q_gemm_mxfp8_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor,
     _check("fp4q_gemm_mxfp8_mxfp4", lib().fp4q_gemm_mxfp8_mxfp4(
         _ptr(qa), _ptr(sfa), _ptr(qb), _ptr(sfb), M, N, K, _ptr(c), cdt, ldc,
         _status_ptr(status, dev), _stream(dev)))
+    return c
+
+
+def fp4q_moe_mxfp4(xq: torch.Tensor, xsf: torch.Tensor, logits: torch.Tensor,
+                   w13: torch.Tensor, sf13: torch.Tensor, w2: torch.Tensor, sf2: torch.Tensor,
+                   top_k: int, renormalize: bool = True, out_dtype: torch.dtype = torch.bfloat16,
+                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                   status: torch.Tensor | None = None) -> torch.Tensor:
+    """A mixture-of-experts layer for T <= 64 tokens: x in MXFP8 (xq [T, H], xsf
+    swizzled), router logits [T, E], MXFP4 weights w13 [E, 2I, H/2] (gate rows,
+    then up rows) and w2 [E, H, I/2] with swizzled scales; returns [T, H]."""
+    if not xq.is_cuda:
+        raise ValueError("xq must be a CUDA tensor")
+    if xq.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError("xq must be [T, H], w13 [E, 2I, H/2] and w2 [E, H, I/2]")
+    (T, H), (E, I), dev = xq.shape, (w13.shape[0], w13.shape[1] // 2), xq.device
+    _expect(xq, "xq", (T, H), (torch.uint8,), dev)
+    _expect(logits, "logits", (T, E), (torch.float32, torch.bfloat16), dev)
+    _expect(w13, "w13", (E, 2 * I, H // 2), (torch.uint8,), dev)
+    _expect(w2, "w2", (E, H, I // 2), (torch.uint8,), dev)
+    if H % 32 == 0 and I % 32 == 0:
+        _expect_bytes(xsf, "xsf", fp4q_scale_bytes(T, H, 32, SCALE_SWIZZLED), dev)
+        _expect_bytes(sf13, "sf13", fp4q_scale_bytes(E * 2 * I, H, 32, SCALE_SWIZZLED), dev)
+        _expect_bytes(sf2, "sf2", fp4q_scale_bytes(E * H, I, 32, SCALE_SWIZZLED), dev)
+    c, cdt, ldo = _matrix_out(out, T, H, out_dtype, dev)
+    need = int(lib().fp4q_moe_mxfp4_workspace_bytes(T, E, top_k, H, I))
+    if workspace is None:
+        workspace = _u8(need, dev)
+    else:
+        _expect_bytes(workspace, "workspace", need, dev)
+    _check("fp4q_moe_mxfp4", lib().fp4q_moe_mxfp4(
+        _ptr(xq), _ptr(xsf), _ptr(logits), _dtype(logits), _ptr(w13), _ptr(sf13), _ptr(w2),
+        _ptr(sf2), T, E, top_k, H, I, int(bool(renormalize)), _ptr(c), cdt, ldo, _ptr(workspace),
+        workspace.numel(), _status_ptr(status, dev), _stream(dev)))
     return c
 
 

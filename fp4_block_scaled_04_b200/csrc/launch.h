@@ -183,6 +183,23 @@ cudaError_t launch_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const
                                     const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
                                     int c_dtype, int64_t ldc, int *status, const Launch &L);
 
+// A mixture-of-experts layer with MXFP4 weights for a few tokens
+constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTopK = 16;
+struct MoeArgs {
+  const uint8_t *xq, *xsf;
+  const void *logits;
+  int logits_dtype;
+  const uint8_t *w13, *sf13, *w2, *sf2;
+  int64_t T, E, k, H, I;
+  bool renormalize;
+  void *out;
+  int out_dtype;
+  int64_t ldo;
+  int *status;
+};
+size_t moe_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t I);
+cudaError_t launch_moe_mxfp4(const MoeArgs &m, void *workspace, const Launch &L);
+
 // IF4 x NVFP4 in one pass over the split operands: C = RN(RN(acc_fp * a) +
 // RN(acc_int * RN(a * RN(6/7)))), acc_int accumulating both INT4 parts; FP32
 // output, N % 128 == 0

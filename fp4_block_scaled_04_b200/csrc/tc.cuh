@@ -140,7 +140,8 @@ __device__ __forceinline__ constexpr uint32_t idesc_mx4x8(uint32_t n, uint32_t b
 }
 
 // The MMAs of one K-tile of 128 values: the scale tiles of A (128 rows) and B
-// (NSFB tiles of 128 columns) into tensor memory at sfa and sfb, four MMAs.
+// (NSFB tiles of 128 columns; 0: B's are there already) into tensor memory at
+// sfa and sfb, four MMAs.
 template <int NSFB>
 __device__ __forceinline__ void mma_ktile_mx4x8(uint32_t d, uint32_t a_smem, uint32_t b_smem,
                                                 uint32_t sfa_smem, uint32_t sfb_smem,

@@ -582,6 +582,36 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const u
                                   const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
                                   int c_dtype, int64_t ldc, int *status, void *stream);
 
+/* A whole mixture-of-experts layer with MXFP4 weights for a few tokens: the
+ * routing, both products, the activation and the weighted sum, in two kernels.
+ *   p    = softmax of the T x E logits, row by row, in FP32; the top_k largest
+ *          are chosen (ties: the lowest index) and, with renormalize != 0,
+ *          divided by their sum.  -inf masks an expert (NaN counts as -inf);
+ *          an expert of probability 0 is not chosen, so that a row without a
+ *          finite logit chooses none and its output is 0
+ *   a    = x W13_e^T in FP32;  h = MXFP8(silu(a[gate]) * a[up]), rounded as
+ *          fp4q_quantize_mxfp8 with FP4Q_E8M0_CEIL
+ *   out  = RN(sum over the chosen experts, in index order, of p_e (h W2_e^T))
+ *   xq, xsf    x in MXFP8: codes [T, H], scales FP4Q_SCALE_SWIZZLED_128x4
+ *   logits     [T, E] dense, of logits_dtype
+ *   w13, sf13  MXFP4 codes [E, 2I, H/2]: an expert's I gate rows, then its I up
+ *              rows; scales FP4Q_SCALE_SWIZZLED_128x4 of the [E 2I, H] matrix
+ *   w2, sf2    MXFP4 codes [E, H, I/2], scales likewise of the [E H, I] matrix
+ *   out, out_dtype, ldo  [T, ldo] row-major, FP32 or BF16; ldo >= H
+ *   workspace  >= fp4q_moe_mxfp4_workspace_bytes(T, E, top_k, H, I) bytes,
+ *              256-byte aligned; calls that overlap on the GPU need one each
+ *   status     as for fp4q_gemm_mxfp8_mxfp4
+ * Equal calls on one GPU give equal bits.  Shape: 0 <= T <= 64, 1 <= E <= 256,
+ * 1 <= top_k <= min(E, 16), H and I positive multiples of 128.  w13, w2
+ * 32-byte aligned, the other pointers 16; ldo * element size % 16 == 0. */
+size_t fp4q_moe_mxfp4_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I);
+fp4q_status fp4q_moe_mxfp4(const uint8_t *xq, const uint8_t *xsf, const void *logits,
+                           int logits_dtype, const uint8_t *w13, const uint8_t *sf13,
+                           const uint8_t *w2, const uint8_t *sf2, int64_t T, int64_t E,
+                           int64_t top_k, int64_t H, int64_t I, int renormalize, void *out,
+                           int out_dtype, int64_t ldo, void *workspace, size_t ws_bytes,
+                           int *status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

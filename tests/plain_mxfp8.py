@@ -85,3 +85,37 @@ def rmsnorm_backward(g, s, w, rstd, d=None):
     r = rstd[:, None]
     dx = r * (w * g - s * r * r * (w * g * s).mean(1, keepdims=True))
     return (dx if d is None else dx + d), (g * s * r).sum(0)
+
+
+def route(logits, k, renormalize):
+    """[T, E] weights (0 where an expert is not chosen) in float64."""
+    p = np.zeros(logits.shape)
+    for t, row in enumerate(np.asarray(logits, np.float64)):
+        row = np.where(np.isnan(row), -np.inf, row)
+        if row.max() == -np.inf:
+            continue
+        q = np.exp(row - row.max())
+        q /= q.sum()
+        at = [e for e in np.argsort(-row, kind="stable")[:k] if q[e] > 0]
+        p[t, at] = q[at] / (q[at].sum() if renormalize else 1.0)
+    return p
+
+
+def moe(x, p, w13, w2):
+    """Output [T, H], and the bound of a difference that comes from h's codes
+    moving by one step: the sum over one code of p 2^-3 |h| |W2|, at its
+    largest.  x [T, H], p [T, E] float64; w13(e), w2(e) give the weights."""
+    T, H = x.shape
+    out, mag, flip = np.zeros((T, H)), np.zeros((T, H)), np.zeros((T, H))
+    for e in np.nonzero(p.any(0))[0]:
+        a = x @ w13(e).T
+        I = a.shape[1] // 2
+        with np.errstate(over="ignore"):
+            h = a[:, :I] / (1 + np.exp(-a[:, :I])) * a[:, I:]
+        v, ex = quantize(h)
+        hq = v * np.repeat(np.ldexp(1.0, ex), 32, 1)
+        W = w2(e)
+        out += p[:, e:e + 1] * (hq @ W.T)
+        mag += p[:, e:e + 1] * (np.abs(hq) @ np.abs(W).T)
+        flip = np.maximum(flip, p[:, e:e + 1] * np.abs(hq).max(1, keepdims=True) * np.abs(W).max())
+    return out, mag, flip * 2.0 ** -3

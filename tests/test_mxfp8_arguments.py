@@ -91,3 +91,24 @@ def test_gemm(L):
     assert gemm(L, M=1 << 20, N=1 << 29, ldc=1 << 29) == SHAPE
     assert gemm(L, ldc=129) == ALIGN
     assert gemm(L, M=0, qa=None, c=None) == OK and gemm(L, N=0, ldc=0) == OK
+
+
+def moe(L, xq=A, xsf=A, logits=A, ldt=1, w13=A, sf13=A, w2=A, sf2=A, T=5, E=8, k=2, H=256, I=128,
+        renorm=1, out=A, dtype=0, ldo=256, ws=A, n=1 << 30, status=None):
+    return L.fp4q_moe_mxfp4(xq, xsf, logits, ldt, w13, sf13, w2, sf2, T, E, k, H, I, renorm, out,
+                            dtype, ldo, ws, n, status, None)
+
+
+def test_moe(L):
+    assert moe(L, ldt=2) == ARG and moe(L, dtype=2) == ARG and moe(L, ldo=248) == ARG
+    assert moe(L, T=-1) == ARG and moe(L, E=0) == ARG and moe(L, k=0) == ARG and moe(L, k=9) == ARG
+    assert moe(L, T=65) == SHAPE and moe(L, E=257) == SHAPE and moe(L, E=64, k=17) == SHAPE
+    assert moe(L, H=192) == SHAPE and moe(L, I=96) == SHAPE and moe(L, I=0) == SHAPE
+    for p in ("xq", "xsf", "logits", "w13", "sf13", "w2", "sf2", "out"):
+        assert moe(L, **{p: None}) == ARG and moe(L, **{p: ODD}) == ALIGN
+    assert moe(L, w2=ctypes.c_void_p(0x7F0000000010)) == ALIGN      # 32 bytes for the weights
+    assert moe(L, ws=ctypes.c_void_p(0x7F0000000080)) == ALIGN      # 256 for the workspace
+    need = L.fp4q_moe_mxfp4_workspace_bytes(5, 8, 2, 256, 128)
+    assert need > 5 * 2 * 128 and L.fp4q_moe_mxfp4_workspace_bytes(0, 8, 2, 256, 128) == 0
+    assert moe(L, n=need - 1) == WS and moe(L, ws=None) == WS
+    assert moe(L, T=0, xq=None, out=None, ws=None) == OK
