@@ -172,7 +172,8 @@ def _matrix(x: torch.Tensor, name: str = "x"):
 
 
 def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The device's current stream (the raw handle: a Stream object costs 2 us more)."""
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def _check(name: str, status: int):

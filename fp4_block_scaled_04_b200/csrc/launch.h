@@ -74,6 +74,44 @@ inline cudaError_t kernel_setup(KernelSetup &ks, const void *kern, int threads, 
   return ks.err[dev];
 }
 
+// Launches a kernel that may begin while its predecessor in the stream drains
+// (programmatic dependent launch): such a kernel calls begin_dependent() before
+// it touches global memory, which waits for the predecessor's end, so that only
+// its launch and set-up overlap.  cluster > 1 launches clusters of that many CTAs.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), int64_t grid, int threads, int smem, int cluster,
+                             const Launch &L, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+#if defined(__CUDACC__)
+// The device side: lets the successor's CTAs start as SMs become free, then
+// waits until the predecessor is complete and its writes are visible.
+__device__ __forceinline__ void begin_dependent() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// The same in a kernel that reads the predecessor's results by TMA.
+__device__ __forceinline__ void begin_dependent_tma() {
+  begin_dependent();
+  asm volatile("fence.proxy.async;" ::: "memory");
+}
+#endif
+
 // The host-side argument checks of fp4q_quantize_nvfp4 that need no device
 // (enums, shape, alignment, required pointers); FP4Q_OK or the status that
 // call would return.

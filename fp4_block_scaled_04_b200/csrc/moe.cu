@@ -95,10 +95,6 @@ struct Bars {
   }
 };
 
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 __device__ __forceinline__ float load_logit(const void *p, int dtype, int64_t i) {
   return dtype == FP4Q_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i])
                             : static_cast<const float *>(p)[i];
@@ -168,10 +164,9 @@ __device__ __forceinline__ int choose(const void *logits, int dtype, int64_t row
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1)
 gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
-               const __grid_constant__ CUtensorMap map_x, const uint8_t *__restrict__ sfw,
-               const uint8_t *__restrict__ sfx, const void *__restrict__ logits, int logits_dtype,
-               int T, int E, int k, bool renormalize, int KT, int NT, int S, Table tab,
-               int *__restrict__ status) {
+               const __grid_constant__ CUtensorMap map_x, const uint8_t *sfw,
+               const uint8_t *sfx, const void *logits, int logits_dtype, int T, int E, int k, bool renormalize, int KT, int NT, int S, Table tab,
+               int *status) {
   using C = GateUp<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -187,7 +182,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       reinterpret_cast<volatile uint32_t *>(smem_raw + (bars.tmem_slot - raw));
   volatile int *err_ptr = reinterpret_cast<volatile int *>(smem_raw + (bars.err_slot - raw));
   float *part = reinterpret_cast<float *>(smem_raw + (base - raw));   // [2][BN][128]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = S > 1 ? blockIdx.x % S : 0, cl = blockIdx.x / S, ncl = gridDim.x / S;
   const int k0 = KT * rank / S, k1 = KT * (rank + 1) / S;
   const int I = NT * 128;
@@ -203,6 +198,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     bars.init();
     *err_ptr = 0;
   }
+  begin_dependent_tma();
   // ---- routing ----
   for (int e = threadIdx.x; e < E; e += kThreads) s_mask[e] = 0;
   for (int t = warp; t < T; t += kThreads / 32) {
@@ -239,7 +235,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     if (lane == 0) s_active = na;
   }
   __syncthreads();
-  const uint32_t tmem = *slot_ptr;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *slot_ptr, 0);
   const int n_active = s_active, n_units = n_active * NT;
   if (blockIdx.x == 0) {
     for (int a = threadIdx.x; a < n_active; a += kThreads) {
@@ -279,20 +275,22 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int g = 0;
-      for (int u = cl; u < n_units && !*err_ptr; u += ncl) {
-        const int a = u / NT, it = u - a * NT;
-        const int gate = s_expert[a] * 2 * NT + it;       // weight tile of the gate rows
-        const uint8_t *fg = sfw + static_cast<int64_t>(gate) * KT * 512;
-        const uint8_t *fu = fg + static_cast<int64_t>(NT) * KT * 512;
-        for (int kt = k0; kt < k1; ++kt, ++g) {
-          const int s = g % STAGES;
-          if (g >= STAGES && !mbar_wait(bars.empty + 8 * s, (g / STAGES - 1) & 1)) {
-            *err_ptr = 1;
-            break;
-          }
-          const uint32_t st = base + s * C::STAGE_BYTES, bar = bars.full + 8 * s;
+    Ring<STAGES> ring(1);                                 // the first round finds it empty
+    int issued = 0;
+    bool ok = true;
+    for (int u = cl; u < n_units && ok; u += ncl) {
+      const int a = u / NT, it = u - a * NT;
+      // weight tile of the gate rows
+      const int gate = __shfl_sync(0xFFFFFFFFu, s_expert[a] * 2 * NT + it, 0);
+      const uint8_t *fg = sfw + static_cast<int64_t>(gate) * KT * 512;
+      const uint8_t *fu = fg + static_cast<int64_t>(NT) * KT * 512;
+      for (int kt = k0; kt < k1; ++kt, ++issued) {
+        if (!warp_wait(bars.empty + 8 * ring.s, ring.phase)) {
+          ok = false;
+          break;
+        }
+        const uint32_t st = base + ring.s * C::STAGE_BYTES, bar = bars.full + 8 * ring.s;
+        if (elect_one()) {
           mbar_expect_tx(bar, 2 * kWTx + BN * 128 + 3 * 512);
           tma_load_2d(st, &map_w, kt * 128, gate * 128, bar);
           tma_load_2d(st + kWTile, &map_w, kt * 128, (gate + NT) * 128, bar);
@@ -301,51 +299,65 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
           bulk_load(st + C::SF_OFF + 512, fu + static_cast<int64_t>(kt) * 512, 512, bar);
           bulk_load(st + C::SF_OFF + 1024, sfx + static_cast<int64_t>(kt) * 512, 512, bar);
         }
+        __syncwarp();
+        ring.next();
       }
-      // after an error: no copy is in flight when the CTA ends
-      if (*err_ptr)
-        for (int i = g > STAGES ? g - STAGES : 0; i < g; ++i)
-          mbar_wait(bars.full + 8 * (i % STAGES), (i / STAGES) & 1);
+      ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
+    }
+    if (!ok) {
+      *err_ptr = 1;
+      drain_loads<STAGES>(bars.full, issued);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int g = 0, i = 0;
-      for (int u = cl; u < n_units && !*err_ptr; u += ncl, ++i) {
-        const int b = i & 1;
-        if (i >= 2 && !mbar_wait(bars.acc_empty + 8 * b, (i / 2 - 1) & 1)) {
-          *err_ptr = 1;
+    Ring<STAGES> ring(0);
+    int b = 0;                                            // accumulators and their phase
+    uint32_t bphase = 1;
+    bool ok = true;
+    const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
+    const uint64_t dsf = desc_sf(base + C::SF_OFF);
+    constexpr uint32_t idesc = idesc_mx4x8(BN);
+    for (int u = cl; u < n_units && ok; u += ncl) {
+      if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      for (int kt = k0; kt < k1; ++kt) {
+        if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
+          ok = false;
           break;
         }
         tc_fence_after();
-        for (int kt = k0; kt < k1; ++kt, ++g) {
-          const int s = g % STAGES;
-          if (!mbar_wait(bars.full + 8 * s, (g / STAGES) & 1)) {
-            *err_ptr = 1;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = base + s * C::STAGE_BYTES;
-          const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * s, d = tmem + 2 * b * BN;
-          mma_ktile_mx4x8<1>(d, st, st + C::X_OFF, st + C::SF_OFF, st + C::SF_OFF + 1024, sf,
-                             sf + 8, BN, kt != k0);
-          mma_ktile_mx4x8<0>(d + BN, st + kWTile, st + C::X_OFF, st + C::SF_OFF + 512, 0, sf + 4,
-                             sf + 8, BN, kt != k0);
-          tc_commit(bars.empty + 8 * s);
+        const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s, d = tmem + 2 * b * BN;
+        const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
+        if (elect_one()) {
+          // gate and the tokens' scales, then up with the same tokens
+          mma_ktile_mx4x8<1>(d, dw + at, dx + at, dsf + at, dsf + at + 64, sf, sf + 8, 0, idesc,
+                             kt != k0);
+          mma_ktile_mx4x8<0>(d + BN, dw + at + kWTile / 16, dx + at, dsf + at + 32, 0, sf + 4,
+                             sf + 8, 0, idesc, kt != k0);
+          tc_commit(bars.empty + 8 * ring.s);
+          if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
         }
-        tc_commit(bars.acc_full + 8 * b);
+        __syncwarp();
+        ring.next();
       }
-      if (*err_ptr) {                                     // wait for the MMAs in flight
-        tc_commit(bars.drain);
-        mbar_wait(bars.drain, 0);
-      }
+      b ^= 1;
+      if (b == 0) bphase ^= 1;
+      ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
+    }
+    if (!ok) {                                            // wait for the MMAs in flight
+      *err_ptr = 1;
+      if (elect_one()) tc_commit(bars.drain);
+      __syncwarp();
+      warp_wait(bars.drain, 0);
     }
   } else {
     const int quarter = warp & 3;
     int i = 0;
-    for (int u = cl; u < n_units && !*err_ptr; u += ncl, ++i) {
+    for (int u = cl; u < n_units; u += ncl, ++i) {
       const int b = i & 1, a = u / NT, it = u - a * NT;
-      const int ok = mbar_wait(bars.acc_full + 8 * b, (i / 2) & 1) ? 1 : 0;
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1)) {
         *err_ptr = 1;
         break;
       }
@@ -388,12 +400,20 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
         if (!((mask >> t) & 1ull)) continue;
         if (j++ % S != rank) continue;
         const uint32_t at = base + (t * 128 + quarter * 32 + lane) * 4;
-        float gate = peer_load(peer_smem(at, 0)), up = peer_load(peer_smem(at + BN * 512, 0));
-        for (int p = 1; p < S; ++p) {
-          gate = __fadd_rn(gate, peer_load(peer_smem(at, p)));
-          up = __fadd_rn(up, peer_load(peer_smem(at + BN * 512, p)));
-        }
-        finish(a, it, quarter, mask, t, gate, up);
+        float gate[8], up[8];
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < S) {
+            gate[p] = peer_load(peer_smem(at, p));
+            up[p] = peer_load(peer_smem(at + BN * 512, p));
+          }
+#pragma unroll
+        for (int p = 1; p < 8; ++p)
+          if (p < S) {
+            gate[0] = __fadd_rn(gate[0], gate[p]);
+            up[0] = __fadd_rn(up[0], up[p]);
+          }
+        finish(a, it, quarter, mask, t, gate[0], up[0]);
       }
     }
     cluster_sync();                                       // no CTA leaves while it is read
@@ -407,14 +427,11 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
                  : "memory");
 }
 
-__device__ __forceinline__ void put(float *p, float v) { *p = v; }
-__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
 template <typename OutT, int BN>
 __global__ void __launch_bounds__(kThreads, Down<BN>::PER_SM)
 down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
-            const uint8_t *__restrict__ sfw, Table tab, int T, int KT, int NT, int S,
-            OutT *__restrict__ out, int64_t ldo, int *__restrict__ status) {
+            const uint8_t *sfw, Table tab, int T, int KT, int NT, int S, OutT *out, int64_t ldo,
+            int *status) {
   using C = Down<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -428,7 +445,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       reinterpret_cast<volatile uint32_t *>(smem_raw + (bars.tmem_slot - raw));
   volatile int *err_ptr = reinterpret_cast<volatile int *>(smem_raw + (bars.err_slot - raw));
   float *sum = reinterpret_cast<float *>(smem_raw + (sums - raw));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = blockIdx.x % S, nt = blockIdx.x / S;
 
   if (warp == 0) {
@@ -442,6 +459,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
     bars.init();
     *err_ptr = 0;
   }
+  begin_dependent_tma();
   const int n_active = *tab.n_active;
   int rows = 0;                                           // rows of h
   for (int a = threadIdx.x; a < n_active; a += kThreads) {
@@ -455,75 +473,97 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *slot_ptr;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *slot_ptr, 0);
   // this CTA's part of the list of (expert, K-tile), expert by expert
   const int total = n_active * KT;
   const int lo = static_cast<int>(static_cast<int64_t>(total) * rank / S);
   const int hi = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / S);
 
   if (warp == 0) {
-    if (lane == 0) {
-      int g = 0;
-      for (int x = lo; x < hi && !*err_ptr; ++x, ++g) {
-        const int a = x / KT, kt = x - a * KT, s = g % STAGES;
-        const int nb = (__popcll(s_mask[a]) + 15) / 16;   // boxes of 16 rows of h
-        if (g >= STAGES && !mbar_wait(bars.empty + 8 * s, (g / STAGES - 1) & 1)) {
-          *err_ptr = 1;
+    Ring<STAGES> ring(1);                                 // the first round finds it empty
+    int issued = 0;
+    bool ok = true;
+    for (int x = lo; x < hi && ok;) {
+      const int a = x / KT, k0 = x - a * KT, k1 = min(KT, k0 + hi - x);
+      const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(s_mask[a]) + 15) / 16, 0);
+      const int h0 = __shfl_sync(0xFFFFFFFFu, s_offset[a], 0);
+      const int wt = __shfl_sync(0xFFFFFFFFu, s_expert[a], 0) * NT + nt;   // weight tile
+      const uint8_t *fw = sfw + static_cast<int64_t>(wt) * KT * 512;
+      const uint8_t *fh = tab.hsf + static_cast<int64_t>(a) * KT * 512;
+      for (int kt = k0; kt < k1; ++kt, ++issued) {
+        if (!warp_wait(bars.empty + 8 * ring.s, ring.phase)) {
+          ok = false;
           break;
         }
-        const uint32_t st = base + s * C::STAGE_BYTES, bar = bars.full + 8 * s;
-        const int wt = s_expert[a] * NT + nt;             // weight tile
-        mbar_expect_tx(bar, kWTx + nb * 2048 + 2 * 512);
-        tma_load_2d(st, &map_w, kt * 128, wt * 128, bar);
-        for (int i = 0; i < nb; ++i)
-          tma_load_2d(st + C::X_OFF + 2048 * i, &map_h, kt * 128, s_offset[a] + 16 * i, bar);
-        bulk_load(st + C::SF_OFF, sfw + (static_cast<int64_t>(wt) * KT + kt) * 512, 512, bar);
-        bulk_load(st + C::SF_OFF + 512, tab.hsf + (static_cast<int64_t>(a) * KT + kt) * 512, 512,
-                  bar);
+        const uint32_t st = base + ring.s * C::STAGE_BYTES, bar = bars.full + 8 * ring.s;
+        if (elect_one()) {
+          mbar_expect_tx(bar, kWTx + nb * 2048 + 2 * 512);
+          tma_load_2d(st, &map_w, kt * 128, wt * 128, bar);
+          for (int i = 0; i < nb; ++i)                    // boxes of 16 rows of h
+            tma_load_2d(st + C::X_OFF + 2048 * i, &map_h, kt * 128, h0 + 16 * i, bar);
+          bulk_load(st + C::SF_OFF, fw + static_cast<int64_t>(kt) * 512, 512, bar);
+          bulk_load(st + C::SF_OFF + 512, fh + static_cast<int64_t>(kt) * 512, 512, bar);
+        }
+        __syncwarp();
+        ring.next();
       }
-      // after an error: no copy is in flight when the CTA ends
-      if (*err_ptr)
-        for (int i = g > STAGES ? g - STAGES : 0; i < g; ++i)
-          mbar_wait(bars.full + 8 * (i % STAGES), (i / STAGES) & 1);
+      x += k1 - k0;
+      ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
+    }
+    if (!ok) {
+      *err_ptr = 1;
+      drain_loads<STAGES>(bars.full, issued);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int i = 0;                                          // experts begun
-      for (int x = lo, g = 0; x < hi && !*err_ptr; ++x, ++g) {
-        const int a = x / KT, kt = x - a * KT, s = g % STAGES, b = i & 1;
-        const bool first = x == lo || kt == 0;
-        if (first && i >= 2 && !mbar_wait(bars.acc_empty + 8 * b, (i / 2 - 1) & 1)) {
-          *err_ptr = 1;
-          break;
-        }
-        if (!mbar_wait(bars.full + 8 * s, (g / STAGES) & 1)) {
-          *err_ptr = 1;
+    Ring<STAGES> ring(0);
+    int b = 0;                                            // accumulator and its phase
+    uint32_t bphase = 1;
+    bool ok = true;
+    const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
+    const uint64_t dsf = desc_sf(base + C::SF_OFF);
+    for (int x = lo; x < hi && ok;) {
+      const int a = x / KT, k0 = x - a * KT, k1 = min(KT, k0 + hi - x);
+      const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(s_mask[a]) + 15) / 16, 0);
+      const uint32_t idesc = idesc_mx4x8(16 * nb);
+      if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      for (int kt = k0; kt < k1; ++kt) {
+        if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
+          ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t n = 16u * ((__popcll(s_mask[a]) + 15) / 16);
-        const uint32_t st = base + s * C::STAGE_BYTES;
-        const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * s;
-        mma_ktile_mx4x8<1>(tmem + b * BN, st, st + C::X_OFF, st + C::SF_OFF, st + C::SF_OFF + 512,
-                           sf, sf + 4, n, !first);
-        tc_commit(bars.empty + 8 * s);
-        if (kt == KT - 1 || x == hi - 1) {
-          tc_commit(bars.acc_full + 8 * b);
-          ++i;
+        const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s;
+        const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
+        if (elect_one()) {
+          mma_ktile_mx4x8<1>(tmem + b * BN, dw + at, dx + at, dsf + at, dsf + at + 32, sf, sf + 4,
+                             0, idesc, kt != k0);
+          tc_commit(bars.empty + 8 * ring.s);
+          if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
         }
+        __syncwarp();
+        ring.next();
       }
-      if (*err_ptr) {                                     // wait for the MMAs in flight
-        tc_commit(bars.drain);
-        mbar_wait(bars.drain, 0);
-      }
+      x += k1 - k0;
+      b ^= 1;
+      if (b == 0) bphase ^= 1;
+      ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
+    }
+    if (!ok) {                                            // wait for the MMAs in flight
+      *err_ptr = 1;
+      if (elect_one()) tc_commit(bars.drain);
+      __syncwarp();
+      warp_wait(bars.drain, 0);
     }
   } else if (lo < hi) {
     const int quarter = warp & 3, row = quarter * 32 + lane;
     int i = 0;
-    for (int a = lo / KT; a <= (hi - 1) / KT && !*err_ptr; ++a, ++i) {
+    for (int a = lo / KT; a <= (hi - 1) / KT; ++a, ++i) {
       const int b = i & 1;
-      const int ok = mbar_wait(bars.acc_full + 8 * b, (i / 2) & 1) ? 1 : 0;
-      if (!__all_sync(0xFFFFFFFFu, ok)) {
+      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1)) {
         *err_ptr = 1;
         break;
       }
@@ -551,15 +591,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
   }
   __syncwarp();
   cluster_sync();
-  if (warp >= 2) {
-    const int row = threadIdx.x - 64;
-    for (int t = rank; t < T; t += S) {
-      const uint32_t at = sums + (t * 128 + row) * 4;
-      float v = peer_load(peer_smem(at, 0));
-      for (int p = 1; p < S; ++p) v = __fadd_rn(v, peer_load(peer_smem(at, p)));
-      put(out + t * ldo + nt * 128 + row, v);
-    }
-  }
+  cluster_sum(sums, T, S, rank, warp, kThreads / 32, lane, out + nt * 128, ldo);
   cluster_sync();                                         // no CTA leaves while it is read
   tc_fence_before();
   __syncthreads();
@@ -585,23 +617,6 @@ struct Layout {
   }
 };
 
-template <typename K, typename... A>
-cudaError_t launch(K kern, int64_t grid, int S, int smem, const Launch &L, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = L.stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(S);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = S > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <typename OutT, int BN>
 cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   static KernelSetup setup1, setup2;
@@ -625,17 +640,16 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   const int64_t most = (m.T * m.k < m.E ? m.T * m.k : m.E) * NT1;
   int S = 1;
   while (S < 8 && most * S * 2 <= L.num_sms && KT1 >= 4 * S) S *= 2;
-  e = launch(k1, S > 1 ? most * S : most < L.num_sms ? most : L.num_sms, S,
-             GateUp<BN>::SMEM_BYTES, L, w13, x, m.sf13, m.xsf, m.logits, m.logits_dtype,
-             static_cast<int>(m.T), static_cast<int>(m.E), static_cast<int>(m.k), m.renormalize,
-             KT1, NT1, S, tab, m.status);
+  e = launch_dependent(k1, S > 1 ? most * S : most < L.num_sms ? most : L.num_sms, kThreads,
+                       GateUp<BN>::SMEM_BYTES, S, L, w13, x, m.sf13, m.xsf, m.logits,
+                       m.logits_dtype, m.T, m.E, m.k, m.renormalize, KT1, NT1, S, tab, m.status);
   if (e != cudaSuccess) return e;
   // second product: the largest cluster that leaves every cluster its place
   const int64_t tiles = m.H / 128, slots = static_cast<int64_t>(L.num_sms) * Down<BN>::PER_SM;
   S = 1;
   while (S < 8 && tiles * S * 2 <= slots) S *= 2;
-  return launch(k2, tiles * S, S, Down<BN>::SMEM_BYTES, L, w2, h, m.sf2, tab,
-                static_cast<int>(m.T), NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo, m.status);
+  return launch_dependent(k2, tiles * S, kThreads, Down<BN>::SMEM_BYTES, S, L, w2, h, m.sf2, tab,
+                          m.T, NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo, m.status);
 }
 
 }  // namespace

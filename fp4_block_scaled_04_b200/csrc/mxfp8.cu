@@ -22,6 +22,7 @@ template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads)
 mxfp8_kernel(const T *__restrict__ x, I rows, I cols, I ld, int mode, uint8_t *__restrict__ q,
              uint8_t *__restrict__ sf, int scale_layout, I srows, I scols) {
+  begin_dependent();
   const I bpr = cols / 32, nblk = srows * scols;
   const I stride = static_cast<I>(gridDim.x) * kThreads;
   for (I b = static_cast<I>(blockIdx.x) * kThreads + threadIdx.x; b < nblk; b += stride) {
@@ -60,6 +61,7 @@ template <typename OutT, typename I>
 __global__ void __launch_bounds__(kThreads)
 mxfp8_dequant_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ sf,
                      int scale_layout, I rows, I cols, OutT *__restrict__ y) {
+  begin_dependent();
   const I upr = cols / 8, n = rows * upr;
   const I scols = static_cast<I>(scale_cols(cols / 32, scale_layout));
   const I stride = static_cast<I>(gridDim.x) * kThreads;
@@ -111,13 +113,10 @@ cudaError_t launch_q(const void *x, int64_t rows, int64_t cols, int64_t ld, int 
   const int grid = grid_for(sr * sc, L);
   const T *p = static_cast<const T *>(x);
   if (narrow(sr * (ld > sc * 32 ? ld : sc * 32), int64_t{grid} * kThreads * 32))
-    mxfp8_kernel<T, uint32_t><<<grid, kThreads, 0, L.stream>>>(
-        p, static_cast<uint32_t>(rows), static_cast<uint32_t>(cols), static_cast<uint32_t>(ld),
-        mode, q, sf, layout, static_cast<uint32_t>(sr), static_cast<uint32_t>(sc));
-  else
-    mxfp8_kernel<T, int64_t><<<grid, kThreads, 0, L.stream>>>(p, rows, cols, ld, mode, q, sf,
-                                                              layout, sr, sc);
-  return cudaGetLastError();
+    return launch_dependent(mxfp8_kernel<T, uint32_t>, grid, kThreads, 0, 1, L, p, rows, cols, ld,
+                            mode, q, sf, layout, sr, sc);
+  return launch_dependent(mxfp8_kernel<T, int64_t>, grid, kThreads, 0, 1, L, p, rows, cols, ld,
+                          mode, q, sf, layout, sr, sc);
 }
 
 template <typename OutT>
@@ -126,12 +125,10 @@ cudaError_t launch_dq(const uint8_t *q, const uint8_t *sf, int layout, int64_t r
   const int grid = grid_for(rows * (cols / 8), L);
   OutT *o = static_cast<OutT *>(y);
   if (narrow((rows + 127) * (cols + 127), int64_t{grid} * kThreads * 8))
-    mxfp8_dequant_kernel<OutT, uint32_t><<<grid, kThreads, 0, L.stream>>>(
-        q, sf, layout, static_cast<uint32_t>(rows), static_cast<uint32_t>(cols), o);
-  else
-    mxfp8_dequant_kernel<OutT, int64_t><<<grid, kThreads, 0, L.stream>>>(q, sf, layout, rows,
-                                                                         cols, o);
-  return cudaGetLastError();
+    return launch_dependent(mxfp8_dequant_kernel<OutT, uint32_t>, grid, kThreads, 0, 1, L, q, sf,
+                            layout, rows, cols, o);
+  return launch_dependent(mxfp8_dequant_kernel<OutT, int64_t>, grid, kThreads, 0, 1, L, q, sf,
+                          layout, rows, cols, o);
 }
 
 }  // namespace

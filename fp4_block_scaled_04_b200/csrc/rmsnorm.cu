@@ -98,6 +98,7 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
                T *sum_out, T *__restrict__ y_out) {
   constexpr int NW = W < 4 ? 4 : W;
   __shared__ float slot[NW];
+  begin_dependent();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (NW / W) + warp / W;
   const int n8 = cols / 8, bpr = cols / 32;
@@ -182,22 +183,22 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
   auto go = [&](auto w, auto v) {
     constexpr int W = decltype(w)::value, VPT = decltype(v)::value, NW = W < 4 ? 4 : W;
     const int64_t grid = (srows + NW / W - 1) / (NW / W);
-    rmsnorm_kernel<T, TW, W, VPT><<<static_cast<unsigned>(grid), NW * 32, 0, L.stream>>>(
-        static_cast<const T *>(x), rows, static_cast<int>(cols), ld, static_cast<const T *>(res),
-        ld_res, static_cast<const TW *>(weight), eps, mode, q, sf, layout, rstd,
-        static_cast<T *>(sum), static_cast<T *>(y));
+    return launch_dependent(rmsnorm_kernel<T, TW, W, VPT>, grid, NW * 32, 0, 1, L,
+                            static_cast<const T *>(x), rows, static_cast<int>(cols), ld,
+                            static_cast<const T *>(res), ld_res, static_cast<const TW *>(weight),
+                            eps, mode, q, sf, layout, rstd, static_cast<T *>(sum),
+                            static_cast<T *>(y));
   };
   using std::integral_constant;
   // the fewest warps that hold the row in two vectors a thread; rows beyond
   // 32 warps take four
-  if (n8 <= 64) go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  else if (n8 <= 128) go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-  else if (n8 <= 256) go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  else if (n8 <= 512) go(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  else if (n8 <= 1024) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  else if (n8 <= 2048) go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  else go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
-  return cudaGetLastError();
+  if (n8 <= 64) return go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+  if (n8 <= 128) return go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
+  if (n8 <= 256) return go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  if (n8 <= 512) return go(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+  if (n8 <= 1024) return go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  if (n8 <= 2048) return go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  return go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
 }
 
 // Backward: a CTA walks the rows blockIdx.x, + gridDim.x, ... and keeps its
@@ -215,6 +216,7 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s,
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
   extern __shared__ float dw[];                          // [G][cols]
   __shared__ float slot[2][NW];
+  begin_dependent();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
   const int n8 = cols / 8;
   float *mine = dw + grp * cols;
@@ -312,6 +314,7 @@ dweight_kernel(const float *__restrict__ part, int parts, int cols, float *__res
   __shared__ float t[8][32];
   const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;                  // cols % 32 == 0
+  begin_dependent();
   float a = 0.0f;
   for (int p = strand; p < parts; p += 8) a += part[static_cast<int64_t>(p) * cols + c];
   t[strand][lane] = a;
@@ -340,15 +343,14 @@ cudaError_t launch_bwd_t(const void *dy, int64_t ld_dy, const void *s, int64_t l
   int64_t grid = static_cast<int64_t>(L.num_sms) * per_sm;
   if (grid > kNormParts) grid = kNormParts;
   if (grid > steps) grid = steps;
-  kern<<<static_cast<unsigned>(grid), NW * 32, 4 * G * cols, L.stream>>>(
-      static_cast<const T *>(dy), ld_dy, static_cast<const T *>(s), ld_s,
-      static_cast<const TW *>(weight), rstd, static_cast<const T *>(dsum), ld_dsum, rows,
-      static_cast<int>(cols), static_cast<T *>(dx), part);
-  e = cudaGetLastError();
+  e = launch_dependent(kern, grid, NW * 32, static_cast<int>(4 * G * cols), 1, L,
+                       static_cast<const T *>(dy), ld_dy, static_cast<const T *>(s), ld_s,
+                       static_cast<const TW *>(weight), rstd, static_cast<const T *>(dsum),
+                       ld_dsum, rows, static_cast<int>(cols), static_cast<T *>(dx), part);
   if (e != cudaSuccess) return e;
-  dweight_kernel<<<static_cast<unsigned>(cols / 32), 256, 0, L.stream>>>(
-      part, static_cast<int>(grid), static_cast<int>(cols), dweight);
-  return cudaGetLastError();
+  return launch_dependent(dweight_kernel, cols / 32, 256, 0, 1, L,
+                          static_cast<const float *>(part), static_cast<int>(grid),
+                          static_cast<int>(cols), dweight);
 }
 
 template <typename T, typename TW>

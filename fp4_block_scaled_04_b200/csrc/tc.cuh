@@ -89,6 +89,22 @@ __device__ __forceinline__ void tc_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// 32 consecutive columns
+__device__ __forceinline__ void tc_load32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
@@ -133,28 +149,80 @@ __device__ __forceinline__ void tc_mma_mx4x8(uint32_t d, uint64_t a, uint64_t b,
 
 // Its instruction descriptor for M = 128 and N columns: A E2M1 (format 5 in
 // bits 7-9), B E4M3 (format 0 in bits 10-12), N / 8 in bits 17-22, E8M0 scales
-// (bit 23), M / 16 from bit 24; `byte` (0..3) is the scale byte of this K step
-// for A (bits 29-30) and B (bits 4-5).
-__device__ __forceinline__ constexpr uint32_t idesc_mx4x8(uint32_t n, uint32_t byte) {
-  return (5u << 7) | ((n >> 3) << 17) | (1u << 23) | (8u << 24) | (byte << 29) | (byte << 4);
+// (bit 23), M / 16 from bit 24; the scale byte (0..3) of a K step goes into bits
+// 29-30 for A and 4-5 for B.
+__device__ __forceinline__ constexpr uint32_t idesc_mx4x8(uint32_t n) {
+  return (5u << 7) | ((n >> 3) << 17) | (1u << 23) | (8u << 24);
+}
+
+// One lane of a converged warp.  The loads, copies, MMAs and commits are issued
+// by a whole warp that runs its loop together and elects a lane per group of
+// instructions: their operands then stay in uniform registers.  A loop that one
+// lane runs alone pays 60-80 cycles for each such instruction (measured: 530
+// cycles to issue two copies, four MMAs and a commit).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)::"memory");
+  return r != 0;
+}
+
+// mbar_wait by a converged warp, the same answer in every lane; the clock is
+// read only when the phase has not completed yet.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))
+    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitCycles)) return false;
+  return true;
 }
 
 // The MMAs of one K-tile of 128 values: the scale tiles of A (128 rows) and B
 // (NSFB tiles of 128 columns; 0: B's are there already) into tensor memory at
-// sfa and sfb, four MMAs.
+// sfa and sfb, four MMAs; B's first column has its scales `skip` columns of
+// tensor memory (32 tokens each) into its tiles.  Issued by one elected lane.
 template <int NSFB>
-__device__ __forceinline__ void mma_ktile_mx4x8(uint32_t d, uint32_t a_smem, uint32_t b_smem,
-                                                uint32_t sfa_smem, uint32_t sfb_smem,
-                                                uint32_t sfa, uint32_t sfb, uint32_t n,
+__device__ __forceinline__ void mma_ktile_mx4x8(uint32_t d, uint64_t da, uint64_t db,
+                                                uint64_t dsfa, uint64_t dsfb, uint32_t sfa,
+                                                uint32_t sfb, uint32_t skip, uint32_t idesc,
                                                 bool accumulate) {
-  tc_copy_sf(sfa, desc_sf(sfa_smem));
+  tc_copy_sf(sfa, dsfa);
 #pragma unroll
-  for (int h = 0; h < NSFB; ++h) tc_copy_sf(sfb + 4u * h, desc_sf(sfb_smem + 512u * h));
-  const uint64_t da = desc_sw128(a_smem), db = desc_sw128(b_smem);
+  for (int h = 0; h < NSFB; ++h) tc_copy_sf(sfb + 4u * h, dsfb + 32u * h);   // 512 bytes on
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k)                       // 32 values = 32 bytes = 2 units
-    tc_mma_mx4x8(d, da + 2u * k, db + 2u * k, idesc_mx4x8(n, k), sfa | (k << 30), sfb | (k << 30),
-                 accumulate || k != 0);
+    tc_mma_mx4x8(d, da + 2u * k, db + 2u * k, idesc | (k << 29) | (k << 4), sfa | (k << 30),
+                 (sfb + skip) | (k << 30), accumulate || k != 0);
+}
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The ring of stages as one role walks it: stage s, and the parity that its
+// barrier has when this round's phase is complete.
+template <int STAGES>
+struct Ring {
+  int s = 0;
+  uint32_t phase;
+  __device__ explicit Ring(uint32_t first) : phase(first) {}
+  __device__ __forceinline__ void next() {
+    if (++s == STAGES) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+// After an error: waits (bounded) until the loads of the last `issued` stages
+// have landed, so that none is in flight when the CTA ends.
+template <int STAGES>
+__device__ __forceinline__ void drain_loads(uint32_t full, int issued) {
+  for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+    warp_wait(full + 8 * (i % STAGES), (i / STAGES) & 1);
 }
 
 // Cluster barrier (every thread of every CTA of the cluster arrives) and
@@ -171,6 +239,48 @@ __device__ __forceinline__ float peer_load(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void put4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  uint2 w;
+  memcpy(&w.x, &a, sizeof(uint32_t));
+  memcpy(&w.y, &b, sizeof(uint32_t));
+  *reinterpret_cast<uint2 *>(p) = w;
+}
+
+// The sum over a cluster of S <= 8 CTAs of their [tokens][128] FP32 parts at
+// shared-memory address `at`, in rank order, to dst[token * ld + row]: tokens in
+// turn over the ranks and the `warps` warps that call this (warp = 0, 1, ...),
+// four rows a lane.  All S loads of a token are in flight together.
+template <typename OutT>
+__device__ __forceinline__ void cluster_sum(uint32_t at, int tokens, int S, int rank, int warp,
+                                            int warps, int lane, OutT *dst, int64_t ld) {
+  uint32_t peer[8];
+#pragma unroll
+  for (int p = 0; p < 8; ++p) peer[p] = peer_smem(at, p < S ? p : 0) + 16 * lane;
+#pragma unroll 2
+  for (int t = rank + S * warp; t < tokens; t += S * warps) {
+    float4 v[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      if (p < S) v[p] = peer_load4(peer[p] + 512 * t);
+#pragma unroll
+    for (int p = 1; p < 8; ++p)
+      if (p < S)
+        v[0] = make_float4(__fadd_rn(v[0].x, v[p].x), __fadd_rn(v[0].y, v[p].y),
+                           __fadd_rn(v[0].z, v[p].z), __fadd_rn(v[0].w, v[p].w));
+    put4(dst + t * ld + 4 * lane, v[0]);
+  }
 }
 
 // cuTensorMapEncodeTiled, reached through the runtime (no link to the driver
@@ -202,7 +312,7 @@ inline bool make_map_mxfp4(CUtensorMap *map, const uint8_t *base, int64_t rows, 
   const cuuint32_t box[2] = {128, 128}, estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<uint8_t *>(base), dims,
              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
 
