@@ -34,7 +34,12 @@
 namespace fp4q {
 namespace {
 
-constexpr int kThreads = 192;                    // producer warp, MMA warp, 4 epilogue warps
+// Seven warps: the producer, two that issue MMAs, four for the epilogue.  A warp
+// needs 40 cycles for each copy, MMA and commit that it issues, about 400 for a
+// weight tile, where the tensor core needs 200: one issuing warp per CTA bounded
+// both kernels (64 tokens, 64 experts: 135 + 61 us).
+constexpr int kThreads = 224;
+constexpr int kMma0 = 1, kMma1 = 6;              // the issuing warps; 2..5 are the epilogue
 constexpr int kWTile = 128 * 128;                // one weight tile in shared memory
 constexpr int kWTx = kWTile / 2;                 // the packed bytes its load counts
 
@@ -50,10 +55,10 @@ struct Table {
 };
 
 template <int BN_> struct GateUp {
-  static constexpr int BN = BN_, STAGES = BN == 64 ? 4 : 5;
+  static constexpr int BN = BN_, STAGES = BN == 16 ? 6 : 5;
   static constexpr int X_OFF = 2 * kWTile, SF_OFF = X_OFF + BN * 128;
   static constexpr int STAGE_BYTES = (SF_OFF + 3 * 512 + 1023) / 1024 * 1024;
-  static constexpr int SF_COL0 = 4 * BN, SF_COLS = 12;   // two buffers of gate and up
+  static constexpr int SF_COL0 = 4 * BN, SF_COLS = 16;   // two buffers of gate and up
   static constexpr int TMEM_COLS = SF_COL0 + STAGES * SF_COLS <= 128   ? 128
                                    : SF_COL0 + STAGES * SF_COLS <= 256 ? 256
                                                                        : 512;
@@ -66,31 +71,34 @@ template <int BN_> struct Down {
   static constexpr int BN = BN_, STAGES = BN == 64 ? 7 : 4, PER_SM = BN == 64 ? 1 : 2;
   static constexpr int X_OFF = kWTile, SF_OFF = X_OFF + BN * 128;
   static constexpr int STAGE_BYTES = (SF_OFF + 2 * 512 + 1023) / 1024 * 1024;
-  static constexpr int SF_COL0 = 2 * BN, SF_COLS = 8;
-  static constexpr int TMEM_COLS = SF_COL0 + STAGES * SF_COLS <= 128 ? 128 : 256;
+  static constexpr int SF_COL0 = 4 * BN, SF_COLS = 8;    // two buffers of two accumulators
+  static constexpr int TMEM_COLS = SF_COL0 + STAGES * SF_COLS <= 128   ? 128
+                                   : SF_COL0 + STAGES * SF_COLS <= 256 ? 256
+                                                                       : 512;
   static constexpr int SUM_BYTES = BN * 512;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SUM_BYTES + 256 + 1024;
-  static_assert(SF_COL0 + STAGES * SF_COLS <= 256, "tensor memory");
+  static_assert(SF_COL0 + STAGES * SF_COLS <= 512 / PER_SM, "tensor memory");
 };
 
 // What a CTA's barriers and slots look like after its stages.
+// readers: the issuing warps that read a stage.
 template <int STAGES>
 struct Bars {
   uint32_t full, empty, acc_full, acc_empty, drain, tmem_slot, err_slot;
   __device__ explicit Bars(uint32_t at)
       : full(at), empty(at + 8 * STAGES), acc_full(at + 16 * STAGES),
         acc_empty(at + 16 * STAGES + 16), drain(at + 16 * STAGES + 32),
-        tmem_slot(at + 16 * STAGES + 40), err_slot(at + 16 * STAGES + 44) {}
-  __device__ void init() const {
+        tmem_slot(at + 16 * STAGES + 48), err_slot(at + 16 * STAGES + 52) {}
+  __device__ void init(int readers) const {
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(empty + 8 * i, readers);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(acc_full + 8 * i, 1);
+      mbar_init(acc_full + 8 * i, 2);                    // both issuing warps
       mbar_init(acc_empty + 8 * i, 4);
+      mbar_init(drain + 8 * i, 1);
     }
-    mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 };
@@ -195,7 +203,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 32) {
-    bars.init();
+    bars.init(2);
     *err_ptr = 0;
   }
   begin_dependent_tma();
@@ -308,13 +316,17 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       *err_ptr = 1;
       drain_loads<STAGES>(bars.full, issued);
     }
-  } else if (warp == 1) {
+  } else if (warp == kMma0 || warp == kMma1) {
+    // one warp multiplies with the gate rows, the other with the up rows; each
+    // copies the scales that it needs to columns of its own
+    const uint32_t w = warp == kMma1;
     Ring<STAGES> ring(0);
     int b = 0;                                            // accumulators and their phase
     uint32_t bphase = 1;
     bool ok = true;
-    const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
-    const uint64_t dsf = desc_sf(base + C::SF_OFF);
+    const uint64_t dw = desc_sw128(base + w * kWTile), dx = desc_sw128(base + C::X_OFF);
+    const uint64_t dsfw = desc_sf(base + C::SF_OFF + 512 * w);
+    const uint64_t dsfx = desc_sf(base + C::SF_OFF + 1024);
     constexpr uint32_t idesc = idesc_mx4x8(BN);
     for (int u = cl; u < n_units && ok; u += ncl) {
       if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
@@ -328,14 +340,11 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
           break;
         }
         tc_fence_after();
-        const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s, d = tmem + 2 * b * BN;
+        const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s + 8 * w;
         const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
         if (elect_one()) {
-          // gate and the tokens' scales, then up with the same tokens
-          mma_ktile_mx4x8<1>(d, dw + at, dx + at, dsf + at, dsf + at + 64, sf, sf + 8, 0, idesc,
-                             kt != k0);
-          mma_ktile_mx4x8<0>(d + BN, dw + at + kWTile / 16, dx + at, dsf + at + 32, 0, sf + 4,
-                             sf + 8, 0, idesc, kt != k0);
+          mma_ktile_mx4x8<1>(tmem + (2 * b + w) * BN, dw + at, dx + at, dsfw + at, dsfx + at, sf,
+                             sf + 4, 0, idesc, kt != k0);
           tc_commit(bars.empty + 8 * ring.s);
           if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
         }
@@ -348,9 +357,9 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     }
     if (!ok) {                                            // wait for the MMAs in flight
       *err_ptr = 1;
-      if (elect_one()) tc_commit(bars.drain);
+      if (elect_one()) tc_commit(bars.drain + 8 * w);
       __syncwarp();
-      warp_wait(bars.drain, 0);
+      warp_wait(bars.drain + 8 * w, 0);
     }
   } else {
     const int quarter = warp & 3;
@@ -392,7 +401,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     // at most one unit per cluster: add the S partial sums, the chosen tokens
     // in turn over the ranks
     cluster_sync();
-    if (warp >= 2 && cl < n_units) {
+    if (warp >= 2 && warp < kMma1 && cl < n_units) {
       const int a = cl / NT, it = cl - a * NT, quarter = warp & 3;
       const unsigned long long mask = s_mask[s_expert[a]];
       int j = 0;
@@ -456,7 +465,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 32) {
-    bars.init();
+    bars.init(1);
     *err_ptr = 0;
   }
   begin_dependent_tma();
@@ -514,15 +523,17 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       *err_ptr = 1;
       drain_loads<STAGES>(bars.full, issued);
     }
-  } else if (warp == 1) {
+  } else if (warp == kMma0 || warp == kMma1) {
+    // the K-tiles of an expert in turn, each warp into an accumulator of its own
+    const int w = warp == kMma1;
     Ring<STAGES> ring(0);
-    int b = 0;                                            // accumulator and its phase
+    int b = 0;                                            // accumulators and their phase
     uint32_t bphase = 1;
     bool ok = true;
     const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
     const uint64_t dsf = desc_sf(base + C::SF_OFF);
     for (int x = lo; x < hi && ok;) {
-      const int a = x / KT, k0 = x - a * KT, k1 = min(KT, k0 + hi - x);
+      const int a = x / KT, k0 = x - a * KT, n = min(KT - k0, hi - x);
       const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(s_mask[a]) + 15) / 16, 0);
       const uint32_t idesc = idesc_mx4x8(16 * nb);
       if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
@@ -530,7 +541,8 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
         break;
       }
       tc_fence_after();
-      for (int kt = k0; kt < k1; ++kt) {
+      for (int i = 0; i < n; ++i, ring.next()) {
+        if ((i & 1) != w) continue;
         if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
           ok = false;
           break;
@@ -539,24 +551,25 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
         const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s;
         const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
         if (elect_one()) {
-          mma_ktile_mx4x8<1>(tmem + b * BN, dw + at, dx + at, dsf + at, dsf + at + 32, sf, sf + 4,
-                             0, idesc, kt != k0);
+          mma_ktile_mx4x8<1>(tmem + (2 * b + w) * BN, dw + at, dx + at, dsf + at, dsf + at + 32,
+                             sf, sf + 4, 0, idesc, i >= 2);
           tc_commit(bars.empty + 8 * ring.s);
-          if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
+          if (i + 2 >= n) tc_commit(bars.acc_full + 8 * b);
         }
         __syncwarp();
-        ring.next();
       }
-      x += k1 - k0;
+      if (w == 1 && n == 1 && lane == 0) mbar_arrive(bars.acc_full + 8 * b);   // nothing to add
+      __syncwarp();
+      x += n;
       b ^= 1;
       if (b == 0) bphase ^= 1;
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
     if (!ok) {                                            // wait for the MMAs in flight
       *err_ptr = 1;
-      if (elect_one()) tc_commit(bars.drain);
+      if (elect_one()) tc_commit(bars.drain + 8 * w);
       __syncwarp();
-      warp_wait(bars.drain, 0);
+      warp_wait(bars.drain + 8 * w, 0);
     }
   } else if (lo < hi) {
     const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -570,12 +583,19 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       tc_fence_after();
       unsigned long long mask = s_mask[a];
       const float *w = s_weight + s_offset[a];
-      const uint32_t acc = tmem + b * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t acc = tmem + 2 * b * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+      // one K-tile alone is all in the first accumulator
+      const bool two = min((a + 1) * KT, hi) - max(a * KT, lo) > 1;
 #pragma unroll 1
       for (int j = 0; mask != 0; j += 16) {
-        uint32_t r[16];
+        uint32_t r[16], r1[16];
         tc_load16(acc + j, r);
+        tc_load16(acc + BN + j, r1);
         tc_wait_ld();
+        if (two)
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            r[q] = __float_as_uint(__fadd_rn(__uint_as_float(r[q]), __uint_as_float(r1[q])));
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           if (mask == 0) continue;
