@@ -898,7 +898,7 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const u
 
 size_t fp4q_moe_mxfp4_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I) {
   if (T <= 0 || E <= 0 || top_k <= 0 || H <= 0 || I <= 0) return 0;
-  return moe_workspace_bytes(T, E, top_k, I);
+  return moe_workspace_bytes(T, E, top_k, H, I);
 }
 
 fp4q_status fp4q_moe_mxfp4(const uint8_t *xq, const uint8_t *xsf, const void *logits,

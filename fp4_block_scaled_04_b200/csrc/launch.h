@@ -235,7 +235,7 @@ struct MoeArgs {
   int64_t ldo;
   int *status;
 };
-size_t moe_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t I);
+size_t moe_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I);
 cudaError_t launch_moe_mxfp4(const MoeArgs &m, void *workspace, const Launch &L);
 
 // IF4 x NVFP4 in one pass over the split operands: C = RN(RN(acc_fp * a) +

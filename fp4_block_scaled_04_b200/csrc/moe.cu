@@ -9,23 +9,28 @@
 // quantizer's default), all sums FP32.
 //
 // Bound by HBM: every chosen expert's weights are read once (at 4.25 bits a
-// value) and nothing else is large.  As in gemm_mx.cu the weights take the
-// MMA's 128 lanes and the tokens its columns, which has two uses here.  The
-// first product runs ALL T tokens against every chosen expert -- up to 64
-// columns cost no more than the weights' own pass through shared memory -- so
-// that no token is gathered, and only the chosen columns go on.  The second
-// product reads the rows of h, which the first kernel wrote sorted by expert.
+// value) and nothing else is large; next to that by shared memory, which each
+// weight passes twice in its 8-bit container.  As in gemm_mx.cu the weights take
+// the MMA's 128 lanes and the tokens its columns.
 //
-//   gate_up_kernel: every CTA works out the routing (a few microseconds of
-//     one pass over the logits; cheaper than a kernel of its own), then walks
-//     (expert, 128 columns of h): two accumulators, gate and up, so that the
-//     activation, the block maximum (a warp holds the 32 rows of a block) and
-//     the rounding happen in the thread that reads tensor memory.  CTA 0 also
-//     writes the routing down for the second kernel.
+//   gate_up_kernel walks (expert, 128 columns of h): two accumulators, gate and
+//     up, so that the activation, the block maximum (a warp holds the 32 rows of
+//     a block) and the rounding happen in the thread that reads tensor memory.
+//     It writes the rows of h sorted by expert.
 //   down_kernel: one cluster of S CTAs per 128 output columns; the CTAs share
 //     the list of (expert, K-tile) evenly, weight each expert's product by p
 //     into FP32 sums in shared memory, and add the S sums in rank order.
-// With few units the first kernel splits K over a cluster in the same way.  No
+//
+// Up to 16 tokens these two are all: every CTA of the first works out the routing
+// (one pass over the logits; cheaper than a kernel of its own) and runs all T
+// tokens against every chosen expert, 16 columns, so that nothing is gathered;
+// only the chosen columns go on.  Above, the idle columns would cost more than a
+// third of the time (64 columns for the 8 tokens of an expert: 320 ns a K-tile
+// and SM against 200), so route_kernel works out the routing once and lays the
+// rows of x out by expert.  (A gather by cp.async inside the first kernel took
+// 570 cycles of the gathering warp per K-tile and bounded it.)
+//
+// With few units the first kernel splits K over a cluster as gemm_mx.cu does.  No
 // atomics on values: equal calls give equal bits.
 #include "launch.h"
 #include "mxfp8.cuh"
@@ -34,71 +39,66 @@
 namespace fp4q {
 namespace {
 
-// Seven warps: the producer, two that issue MMAs, four for the epilogue.  A warp
-// needs 40 cycles for each copy, MMA and commit that it issues, about 400 for a
-// weight tile, where the tensor core needs 200: one issuing warp per CTA bounded
-// both kernels (64 tokens, 64 experts: 135 + 61 us).
+// Seven warps: two load (the weights; the tokens), one issues MMAs, four are the
+// epilogue.
 constexpr int kThreads = 224;
-constexpr int kMma0 = 1, kMma1 = 6;              // the issuing warps; 2..5 are the epilogue
+constexpr int kLoadW = 0, kMma = 1, kLoadX = 6;  // 2..5 are the epilogue
 constexpr int kWTile = 128 * 128;                // one weight tile in shared memory
 constexpr int kWTx = kWTile / 2;                 // the packed bytes its load counts
 
-// The routing as the second kernel reads it, and h: parts of the workspace.
+// The routing as the later kernels read it, x by expert and h: parts of the
+// workspace.
 struct Table {
   int *n_active;                                 // chosen experts
   int *expert;                                   // [n_active], ascending
   int *offset;                                   // [n_active] first row of the expert in h
   unsigned long long *mask;                      // [n_active] bit t: token t chose it
   float *weight;                                 // [rows of h]
+  uint8_t *xq;                                   // [T k, H] E4M3 (above 16 tokens)
+  uint8_t *xsf;                                  // [active][H / 128][512] scale tiles
   uint8_t *hq;                                   // [T k, I] E4M3
   uint8_t *hsf;                                  // [active][I / 128][512] scale tiles
 };
 
-template <int BN_> struct GateUp {
-  static constexpr int BN = BN_, STAGES = BN == 16 ? 6 : 5;
-  static constexpr int X_OFF = 2 * kWTile, SF_OFF = X_OFF + BN * 128;
-  static constexpr int STAGE_BYTES = (SF_OFF + 3 * 512 + 1023) / 1024 * 1024;
-  static constexpr int SF_COL0 = 4 * BN, SF_COLS = 16;   // two buffers of gate and up
-  static constexpr int TMEM_COLS = SF_COL0 + STAGES * SF_COLS <= 128   ? 128
-                                   : SF_COL0 + STAGES * SF_COLS <= 256 ? 256
-                                                                       : 512;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 256 + 1024;
-  static_assert(SF_COL0 + STAGES * SF_COLS <= 512, "tensor memory");
-  static_assert(BN * 1024 <= STAGES * STAGE_BYTES, "partial sums fit the stages");
-};
-
-template <int BN_> struct Down {
-  static constexpr int BN = BN_, STAGES = BN == 64 ? 7 : 4, PER_SM = BN == 64 ? 1 : 2;
+// One stage: a weight tile, up to BN rows of tokens, a scale tile of each.  BN is
+// the most tokens (so the most columns) of an expert.
+template <int BN_, int STAGES_, int PER_SM_, int ACCS, int EXTRA> struct Stages {
+  static constexpr int BN = BN_, STAGES = STAGES_, PER_SM = PER_SM_;
   static constexpr int X_OFF = kWTile, SF_OFF = X_OFF + BN * 128;
   static constexpr int STAGE_BYTES = (SF_OFF + 2 * 512 + 1023) / 1024 * 1024;
-  static constexpr int SF_COL0 = 4 * BN, SF_COLS = 8;    // two buffers of two accumulators
-  static constexpr int TMEM_COLS = SF_COL0 + STAGES * SF_COLS <= 128   ? 128
-                                   : SF_COL0 + STAGES * SF_COLS <= 256 ? 256
-                                                                       : 512;
-  static constexpr int SUM_BYTES = BN * 512;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + SUM_BYTES + 256 + 1024;
-  static_assert(SF_COL0 + STAGES * SF_COLS <= 512 / PER_SM, "tensor memory");
+  static constexpr int SF_COL0 = ACCS * BN, SF_COLS = 8, COLS = SF_COL0 + STAGES * SF_COLS;
+  static constexpr int TMEM_COLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static constexpr int EXTRA_BYTES = EXTRA;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EXTRA + 256 + 1024;
+  static_assert(TMEM_COLS <= 512 / PER_SM, "tensor memory");
+  static_assert(BN * 1024 <= STAGES * STAGE_BYTES, "partial sums fit the stages");
 };
+// the first product: two buffers of gate and up
+template <int BN>
+using GateUp = Stages<BN, BN == 64 ? 8 : BN == 32 ? 4 : 5, BN == 64 ? 1 : 2, 4, 0>;
+// the second: two accumulators, and the FP32 sums [BN][128]
+template <int BN>
+using Down = Stages<BN, BN == 64 ? 7 : 4, BN == 64 ? 1 : 2, 2, BN * 512>;
 
 // What a CTA's barriers and slots look like after its stages.
-// readers: the issuing warps that read a stage.
 template <int STAGES>
 struct Bars {
   uint32_t full, empty, acc_full, acc_empty, drain, tmem_slot, err_slot;
   __device__ explicit Bars(uint32_t at)
       : full(at), empty(at + 8 * STAGES), acc_full(at + 16 * STAGES),
         acc_empty(at + 16 * STAGES + 16), drain(at + 16 * STAGES + 32),
-        tmem_slot(at + 16 * STAGES + 48), err_slot(at + 16 * STAGES + 52) {}
-  __device__ void init(int readers) const {
+        tmem_slot(at + 16 * STAGES + 40), err_slot(at + 16 * STAGES + 44) {}
+  // loaders: what arrives on a stage when it is loaded
+  __device__ void init(int loaders) const {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, readers);
+      mbar_init(full + 8 * i, loaders);
+      mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(acc_full + 8 * i, 2);                    // both issuing warps
+      mbar_init(acc_full + 8 * i, 1);
       mbar_init(acc_empty + 8 * i, 4);
-      mbar_init(drain + 8 * i, 1);
     }
+    mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 };
@@ -115,17 +115,18 @@ __device__ __forceinline__ uint32_t ordered(float v) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// One token's choice by one warp: softmax statistics over E logits (E <= 256,
-// expert lane + 32 i in register i), then k times the largest that is left.
+// One token's choice by one warp: softmax statistics over E <= 32 NI logits (expert
+// lane + 32 i in register i), then k times the largest that is left.
 // An expert whose probability is 0 is not chosen; a row without a finite logit
 // chooses none.  e_sel, w_sel: [k] in shared memory; returns how many.
+template <int NI>
 __device__ __forceinline__ int choose(const void *logits, int dtype, int64_t row, int E, int k,
                                       bool renormalize, int lane, int16_t *e_sel, float *w_sel) {
   constexpr float kNone = -INFINITY;
-  float v[kMoeMaxExperts / 32];
+  float v[NI];
   float top = kNone;
 #pragma unroll
-  for (int i = 0; i < kMoeMaxExperts / 32; ++i) {
+  for (int i = 0; i < NI; ++i) {
     const int e = lane + 32 * i;
     v[i] = e < E ? load_logit(logits, dtype, row * E + e) : kNone;
     if (!(v[i] > kNone)) v[i] = kNone;                   // NaN counts as masked
@@ -136,54 +137,178 @@ __device__ __forceinline__ int choose(const void *logits, int dtype, int64_t row
   if (top == kNone) return 0;
   float sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kMoeMaxExperts / 32; ++i) sum += expf(v[i] - top);
+  for (int i = 0; i < NI; ++i) sum += expf(v[i] - top);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  float total = 0.0f;
-  int n = 0;
-  for (; n < k; ++n) {
+  int mine_e = 0;                                         // lane i keeps the i-th choice
+  float mine_v = kNone;
+  for (int n = 0; n < k; ++n) {
     float best = kNone;
     int at = lane;
 #pragma unroll
-    for (int i = 0; i < kMoeMaxExperts / 32; ++i)
+    for (int i = 0; i < NI; ++i)
       if (v[i] > best) {
         best = v[i];
         at = lane + 32 * i;
       }
     const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, ordered(best));
     const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, ordered(best) == m ? at : 0xFFFFu);
-    const uint32_t b = m & 0x80000000u ? m & 0x7FFFFFFFu : ~m;
-    const float p = __fdiv_rn(expf(__uint_as_float(b) - top), sum);
-    if (!(p > 0.0f)) break;
-    total += p;
-    if (lane == 0) {
-      e_sel[n] = static_cast<int16_t>(e);
-      w_sel[n] = p;
+    if (lane == n) {
+      mine_e = static_cast<int>(e);
+      mine_v = __uint_as_float(m & 0x80000000u ? m & 0x7FFFFFFFu : ~m);
     }
 #pragma unroll
-    for (int i = 0; i < kMoeMaxExperts / 32; ++i)
+    for (int i = 0; i < NI; ++i)
       if (static_cast<uint32_t>(lane + 32 * i) == e) v[i] = kNone;
   }
-  __syncwarp();
-  if (renormalize && lane < n) w_sel[lane] = __fdiv_rn(w_sel[lane], total);   // n <= 16
+  const float p = __fdiv_rn(expf(mine_v - top), sum);     // descending over the lanes
+  const int n = __popc(__ballot_sync(0xFFFFFFFFu, p > 0.0f));
+  float total = p;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);   // k <= 16
+  if (lane < n) {
+    e_sel[lane] = static_cast<int16_t>(mine_e);
+    w_sel[lane] = renormalize ? __fdiv_rn(p, total) : p;
+  }
   return n;
 }
 
-template <int BN>
-__global__ void __launch_bounds__(kThreads, 1)
+// The routing in shared memory.
+struct Routing {
+  unsigned long long mask[kMoeMaxExperts];               // by expert: bit t, token t chose it
+  int16_t expert[kMoeMaxExperts], offset[kMoeMaxExperts];   // by active index
+  int16_t first[kMoeMaxExperts];                         // offset by expert
+  int16_t sel[kMoeMaxTokens * kMoeMaxTopK];              // a token's choices
+  float wsel[kMoeMaxTokens * kMoeMaxTopK];
+  int nsel[kMoeMaxTokens];
+  int active;
+};
+
+// Worked out by all threads of a CTA, which ends with a barrier; `write` puts it
+// into the table.
+__device__ __forceinline__ void route(Routing &r, const void *logits, int logits_dtype, int T,
+                                      int E, int k, bool renormalize, bool write,
+                                      const Table &tab) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
+  for (int e = threadIdx.x; e < E; e += threads) r.mask[e] = 0;
+  auto choices = [&](auto ni) {
+    for (int t = warp; t < T; t += threads / 32) {
+      const int n = choose<decltype(ni)::value>(logits, logits_dtype, t, E, k, renormalize, lane,
+                                                r.sel + t * k, r.wsel + t * k);
+      if (lane == 0) r.nsel[t] = n;
+    }
+  };
+  static_assert(kMoeMaxExperts <= 32 * 8, "choose");
+  if (E <= 32) choices(std::integral_constant<int, 1>{});
+  else if (E <= 64) choices(std::integral_constant<int, 2>{});
+  else if (E <= 128) choices(std::integral_constant<int, 4>{});
+  else choices(std::integral_constant<int, 8>{});
+  __syncthreads();
+  for (int i = threadIdx.x; i < T * k; i += threads)
+    if (i % k < r.nsel[i / k]) atomicOr(&r.mask[r.sel[i]], 1ull << (i / k));
+  __syncthreads();
+  if (warp == 0) {
+    int na = 0, no = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int n = e < E ? __popcll(r.mask[e]) : 0;
+      const uint32_t on = __ballot_sync(0xFFFFFFFFu, n > 0);
+      int sc = n;                                         // inclusive scan of the counts
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xFFFFFFFFu, sc, o);
+        if (lane >= o) sc += up;
+      }
+      if (n > 0) {
+        const int a = na + __popc(on & ((1u << lane) - 1u));
+        r.expert[a] = static_cast<int16_t>(e);
+        r.offset[a] = r.first[e] = static_cast<int16_t>(no + sc - n);
+      }
+      na += __popc(on);
+      no += __shfl_sync(0xFFFFFFFFu, sc, 31);
+    }
+    if (lane == 0) r.active = na;
+  }
+  __syncthreads();
+  if (!write) return;
+  for (int i = threadIdx.x; i < T * k; i += threads) {
+    const int t = i / k, e = r.sel[i];
+    if (i - t * k >= r.nsel[t]) continue;
+    tab.weight[r.first[e] + __popcll(r.mask[e] & ((1ull << t) - 1ull))] = r.wsel[i];
+  }
+  for (int a = threadIdx.x; a < r.active; a += threads) {
+    tab.expert[a] = r.expert[a];
+    tab.offset[a] = r.offset[a];
+    tab.mask[a] = r.mask[r.expert[a]];
+  }
+  if (threadIdx.x == 0) *tab.n_active = r.active;
+}
+
+// The routing, and x by expert: CTA b copies the choices b, b + gridDim.x, ... (a
+// token and one of its experts each): a row of codes, and its scale bytes into
+// the expert's scale tiles.  Every CTA works the routing out for itself: 32 warps
+// do 64 tokens in two turns.
+constexpr int kRouteThreads = 1024;
+__global__ void __launch_bounds__(kRouteThreads)
+route_kernel(const uint8_t *xq, const uint8_t *xsf, const void *logits, int logits_dtype, int T,
+             int E, int k, bool renormalize, int KT, Table tab) {
+  __shared__ Routing r;
+  __shared__ int16_t s_active[kMoeMaxExperts];           // active index by expert
+  begin_dependent();
+  route(r, logits, logits_dtype, T, E, k, renormalize, blockIdx.x == 0, tab);
+  for (int a = threadIdx.x; a < r.active; a += kRouteThreads)
+    s_active[r.expert[a]] = static_cast<int16_t>(a);
+  __syncthreads();
+  // per choice 8 KT chunks of 16 bytes and KT words of scales, all choices of the
+  // CTA in one flat loop
+  const int per = 9 * KT, mine = (T * k - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  const uint32_t *sf = reinterpret_cast<const uint32_t *>(xsf);
+  for (int x = threadIdx.x; x < mine * per; x += kRouteThreads) {
+    const int q = x / per, c = x - q * per;
+    const int i = blockIdx.x + q * gridDim.x, t = i / k, e = r.sel[i];
+    if (i - t * k >= r.nsel[t]) continue;
+    const int j = __popcll(r.mask[e] & ((1ull << t) - 1ull));   // its place with the expert
+    if (c < 8 * KT) {
+      const int64_t row = static_cast<int64_t>(KT) * 8;
+      reinterpret_cast<uint4 *>(tab.xq)[(r.first[e] + j) * row + c] =
+          reinterpret_cast<const uint4 *>(xq)[t * row + c];
+    } else {
+      const int kt = c - 8 * KT;
+      reinterpret_cast<uint32_t *>(tab.xsf)[(static_cast<int64_t>(s_active[e]) * KT + kt) * 128 +
+                                            j % 32 * 4 + j / 32] =
+          sf[static_cast<int64_t>(kt) * 128 + t % 32 * 4 + t / 32];
+    }
+  }
+}
+
+// The table in shared memory, for the kernels that read it.
+struct Chosen {
+  unsigned long long mask[kMoeMaxExperts];               // by active index
+  int16_t expert[kMoeMaxExperts], offset[kMoeMaxExperts];
+  __device__ __forceinline__ int load(const Table &tab) {   // the caller's barrier follows
+    const int n = *tab.n_active;
+    for (int a = threadIdx.x; a < n; a += blockDim.x) {
+      expert[a] = static_cast<int16_t>(tab.expert[a]);
+      offset[a] = static_cast<int16_t>(tab.offset[a]);
+      mask[a] = tab.mask[a];
+    }
+    return n;
+  }
+};
+
+// SORTED: x lies by expert in the table's buffers (map_x reads it in boxes of 16
+// rows); else map_x reads all T rows and the routing is worked out here.
+template <int BN, bool SORTED>
+__global__ void __launch_bounds__(kThreads, GateUp<BN>::PER_SM)
 gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
-               const __grid_constant__ CUtensorMap map_x, const uint8_t *sfw,
-               const uint8_t *sfx, const void *logits, int logits_dtype, int T, int E, int k, bool renormalize, int KT, int NT, int S, Table tab,
+               const __grid_constant__ CUtensorMap map_x, const uint8_t *sfw, const uint8_t *sfx,
+               const void *logits, int logits_dtype, int T, int E, int k, bool renormalize, int KT, int NT, int S, Table tab,
                int *status) {
   using C = GateUp<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ unsigned long long s_mask[kMoeMaxExperts];  // by expert
-  __shared__ int16_t s_expert[kMoeMaxExperts], s_offset[kMoeMaxExperts];   // by active index
-  __shared__ int16_t s_sel[kMoeMaxTokens * kMoeMaxTopK];
-  __shared__ float s_wsel[kMoeMaxTokens * kMoeMaxTopK];
-  __shared__ int s_nsel[kMoeMaxTokens];
-  __shared__ int s_active;
+  __shared__ Chosen ch;
+  __shared__ std::conditional_t<SORTED, int, Routing> s_routing;
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   const Bars<STAGES> bars(base + STAGES * C::STAGE_BYTES);
   volatile uint32_t *slot_ptr =
@@ -207,108 +332,73 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     *err_ptr = 0;
   }
   begin_dependent_tma();
-  // ---- routing ----
-  for (int e = threadIdx.x; e < E; e += kThreads) s_mask[e] = 0;
-  for (int t = warp; t < T; t += kThreads / 32) {
-    const int n = choose(logits, logits_dtype, t, E, k, renormalize, lane, s_sel + t * k,
-                         s_wsel + t * k);
-    if (lane == 0) s_nsel[t] = n;
+  int n_active;
+  if constexpr (SORTED) {
+    n_active = ch.load(tab);
+  } else {
+    Routing &r = s_routing;
+    route(r, logits, logits_dtype, T, E, k, renormalize, blockIdx.x == 0, tab);
+    n_active = r.active;
+    for (int a = threadIdx.x; a < n_active; a += kThreads) {
+      ch.expert[a] = r.expert[a];
+      ch.offset[a] = r.offset[a];
+      ch.mask[a] = r.mask[r.expert[a]];
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  for (int i = threadIdx.x; i < T * k; i += kThreads)
-    if (i % k < s_nsel[i / k]) atomicOr(&s_mask[s_sel[i]], 1ull << (i / k));
-  __syncthreads();
-  if (warp == 0) {
-    int na = 0, no = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + lane;
-      const int n = e < E ? __popcll(s_mask[e]) : 0;
-      const uint32_t on = __ballot_sync(0xFFFFFFFFu, n > 0);
-      int sc = n;                                         // inclusive scan of the counts
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xFFFFFFFFu, sc, o);
-        if (lane >= o) sc += up;
-      }
-      if (n > 0) {
-        const int a = na + __popc(on & ((1u << lane) - 1u));
-        s_expert[a] = static_cast<int16_t>(e);
-        s_offset[a] = static_cast<int16_t>(no + sc - n);
-      }
-      na += __popc(on);
-      no += __shfl_sync(0xFFFFFFFFu, sc, 31);
-    }
-    if (lane == 0) s_active = na;
-  }
-  __syncthreads();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *slot_ptr, 0);
-  const int n_active = s_active, n_units = n_active * NT;
-  if (blockIdx.x == 0) {
-    for (int a = threadIdx.x; a < n_active; a += kThreads) {
-      tab.expert[a] = s_expert[a];
-      tab.offset[a] = s_offset[a];
-      tab.mask[a] = s_mask[s_expert[a]];
-    }
-    for (int i = threadIdx.x; i < T * k; i += kThreads) {
-      const int t = i / k;
-      if (i - t * k >= s_nsel[t]) continue;
-      // the expert's active index: chosen experts below it
-      const int e = s_sel[i];
-      int lo = 0, hi = n_active - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (s_expert[mid] < e) lo = mid + 1;
-        else hi = mid;
-      }
-      tab.weight[s_offset[lo] + __popcll(s_mask[e] & ((1ull << t) - 1ull))] = s_wsel[i];
-    }
-    if (threadIdx.x == 0) *tab.n_active = n_active;
-  }
+  const int n_units = n_active * NT;
 
-  // h of token t at this thread's row of unit (a, it), from its two sums
-  auto finish = [&](int a, int it, int quarter, unsigned long long mask, int t, float gate,
-                    float up) {
+  // h of the expert's j-th token at this thread's row of unit (a, it)
+  auto finish = [&](int a, int it, int quarter, int j, float gate, float up) {
     const float h = __fmul_rn(__fdiv_rn(gate, __fadd_rn(1.0f, expf(-gate))), up);
     const float m =
         __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fabsf(h))));
     const uint32_t byte = e8m0_biased_e4m3(m, FP4Q_E8M0_CEIL);
-    const int j = __popcll(mask & ((1ull << t) - 1ull));  // the token's place with its expert
-    tab.hq[static_cast<int64_t>(s_offset[a] + j) * I + it * 128 + quarter * 32 + lane] =
+    tab.hq[static_cast<int64_t>(ch.offset[a] + j) * I + it * 128 + quarter * 32 + lane] =
         static_cast<uint8_t>(e4m3x2(__fmul_rn(h, e8m0_inverse(byte)), 0.0f));
     if (lane == 0)
       tab.hsf[(static_cast<int64_t>(a) * NT + it) * 512 + j % 32 * 16 + j / 32 * 4 + quarter] =
           static_cast<uint8_t>(byte);
   };
 
-  if (warp == 0) {
+  if (warp == kLoadW || warp == kLoadX) {
+    // one warp loads the weights, the other the tokens, each with its scales
     Ring<STAGES> ring(1);                                 // the first round finds it empty
     int issued = 0;
     bool ok = true;
     for (int u = cl; u < n_units && ok; u += ncl) {
       const int a = u / NT, it = u - a * NT;
-      // weight tile of the gate rows
-      const int gate = __shfl_sync(0xFFFFFFFFu, s_expert[a] * 2 * NT + it, 0);
-      const uint8_t *fg = sfw + static_cast<int64_t>(gate) * KT * 512;
-      const uint8_t *fu = fg + static_cast<int64_t>(NT) * KT * 512;
-      for (int kt = k0; kt < k1; ++kt, ++issued) {
-        if (!warp_wait(bars.empty + 8 * ring.s, ring.phase)) {
-          ok = false;
-          break;
+      // weight tile of the gate rows; the up rows' is NT tiles on
+      int tile = __shfl_sync(0xFFFFFFFFu, ch.expert[a] * 2 * NT + it, 0);
+      const int nb = SORTED ? __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[a]) + 15) / 16, 0) : 1;
+      const int x0 = SORTED ? __shfl_sync(0xFFFFFFFFu, ch.offset[a], 0) : 0;
+      const uint8_t *fx = SORTED ? tab.xsf + static_cast<int64_t>(a) * KT * 512 : sfx;
+      for (int half = 0; half < 2 && ok; ++half, tile += NT) {
+        const uint8_t *fw = sfw + static_cast<int64_t>(tile) * KT * 512;
+        for (int kt = k0; kt < k1; ++kt, ++issued) {
+          if (!warp_wait(bars.empty + 8 * ring.s, ring.phase)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = base + ring.s * C::STAGE_BYTES, bar = bars.full + 8 * ring.s;
+          if (elect_one()) {
+            if (warp == kLoadW) {
+              mbar_expect_tx(bar, kWTx + 512);
+              tma_load_2d(st, &map_w, kt * 128, tile * 128, bar);
+              bulk_load(st + C::SF_OFF, fw + static_cast<int64_t>(kt) * 512, 512, bar);
+            } else {
+              mbar_expect_tx(bar, nb * 2048 + 512);
+              for (int i = 0; i < nb; ++i)                // boxes of 16 rows
+                tma_load_2d(st + C::X_OFF + 2048 * i, &map_x, kt * 128, x0 + 16 * i, bar);
+              bulk_load(st + C::SF_OFF + 512, fx + static_cast<int64_t>(kt) * 512, 512, bar);
+            }
+          }
+          __syncwarp();
+          ring.next();
         }
-        const uint32_t st = base + ring.s * C::STAGE_BYTES, bar = bars.full + 8 * ring.s;
-        if (elect_one()) {
-          mbar_expect_tx(bar, 2 * kWTx + BN * 128 + 3 * 512);
-          tma_load_2d(st, &map_w, kt * 128, gate * 128, bar);
-          tma_load_2d(st + kWTile, &map_w, kt * 128, (gate + NT) * 128, bar);
-          tma_load_2d(st + C::X_OFF, &map_x, kt * 128, 0, bar);
-          bulk_load(st + C::SF_OFF, fg + static_cast<int64_t>(kt) * 512, 512, bar);
-          bulk_load(st + C::SF_OFF + 512, fu + static_cast<int64_t>(kt) * 512, 512, bar);
-          bulk_load(st + C::SF_OFF + 1024, sfx + static_cast<int64_t>(kt) * 512, 512, bar);
-        }
-        __syncwarp();
-        ring.next();
       }
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
@@ -316,40 +406,41 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       *err_ptr = 1;
       drain_loads<STAGES>(bars.full, issued);
     }
-  } else if (warp == kMma0 || warp == kMma1) {
-    // one warp multiplies with the gate rows, the other with the up rows; each
-    // copies the scales that it needs to columns of its own
-    const uint32_t w = warp == kMma1;
+  } else if (warp == kMma) {
+    // the K-tiles with the gate rows, then those with the up rows
     Ring<STAGES> ring(0);
     int b = 0;                                            // accumulators and their phase
     uint32_t bphase = 1;
     bool ok = true;
-    const uint64_t dw = desc_sw128(base + w * kWTile), dx = desc_sw128(base + C::X_OFF);
-    const uint64_t dsfw = desc_sf(base + C::SF_OFF + 512 * w);
-    const uint64_t dsfx = desc_sf(base + C::SF_OFF + 1024);
-    constexpr uint32_t idesc = idesc_mx4x8(BN);
+    const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
+    const uint64_t dsf = desc_sf(base + C::SF_OFF);
     for (int u = cl; u < n_units && ok; u += ncl) {
+      const int nb =
+          SORTED ? __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[u / NT]) + 15) / 16, 0) : 1;
+      const uint32_t idesc = idesc_mx4x8(16 * nb);
       if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      for (int kt = k0; kt < k1; ++kt) {
-        if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
-          ok = false;
-          break;
+      for (int half = 0; half < 2 && ok; ++half) {
+        for (int kt = k0; kt < k1; ++kt) {
+          if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s;
+          const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
+          if (elect_one()) {
+            mma_ktile_mx4x8<1>(tmem + (2 * b + half) * BN, dw + at, dx + at, dsf + at,
+                               dsf + at + 32, sf, sf + 4, 0, idesc, kt != k0);
+            tc_commit(bars.empty + 8 * ring.s);
+            if (half == 1 && kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
+          }
+          __syncwarp();
+          ring.next();
         }
-        tc_fence_after();
-        const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s + 8 * w;
-        const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
-        if (elect_one()) {
-          mma_ktile_mx4x8<1>(tmem + (2 * b + w) * BN, dw + at, dx + at, dsfw + at, dsfx + at, sf,
-                             sf + 4, 0, idesc, kt != k0);
-          tc_commit(bars.empty + 8 * ring.s);
-          if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
-        }
-        __syncwarp();
-        ring.next();
       }
       b ^= 1;
       if (b == 0) bphase ^= 1;
@@ -357,9 +448,9 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     }
     if (!ok) {                                            // wait for the MMAs in flight
       *err_ptr = 1;
-      if (elect_one()) tc_commit(bars.drain + 8 * w);
+      if (elect_one()) tc_commit(bars.drain);
       __syncwarp();
-      warp_wait(bars.drain + 8 * w, 0);
+      warp_wait(bars.drain, 0);
     }
   } else {
     const int quarter = warp & 3;
@@ -371,24 +462,29 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
         break;
       }
       tc_fence_after();
-      const unsigned long long mask = s_mask[s_expert[a]];
+      const unsigned long long mask = ch.mask[a];
       const uint32_t acc = tmem + 2 * b * BN + (static_cast<uint32_t>(quarter * 32) << 16);
+      // the columns to go on: the expert's rows, or the chosen ones of all tokens
+      const unsigned long long on =
+          SORTED ? ~0ull >> (64 - __popcll(mask)) : mask;
+      int j = 0;                                          // the token's place with its expert
 #pragma unroll 1
-      for (int j = 0; j < BN / 16; ++j) {
-        if (((mask >> (16 * j)) & 0xFFFFull) == 0) continue;
+      for (int t0 = 0; t0 < BN; t0 += 16) {
+        if (((on >> t0) & 0xFFFFull) == 0) continue;
         uint32_t rg[16], ru[16];
-        tc_load16(acc + 16 * j, rg);
-        tc_load16(acc + BN + 16 * j, ru);
+        tc_load16(acc + t0, rg);
+        tc_load16(acc + BN + t0, ru);
         tc_wait_ld();
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          const int t = 16 * j + q;
+          if (!((on >> (t0 + q)) & 1ull)) continue;
           if (S > 1) {
-            part[t * 128 + quarter * 32 + lane] = __uint_as_float(rg[q]);
-            part[(BN + t) * 128 + quarter * 32 + lane] = __uint_as_float(ru[q]);
-          } else if ((mask >> t) & 1ull) {
-            finish(a, it, quarter, mask, t, __uint_as_float(rg[q]), __uint_as_float(ru[q]));
+            part[j * 128 + quarter * 32 + lane] = __uint_as_float(rg[q]);
+            part[(BN + j) * 128 + quarter * 32 + lane] = __uint_as_float(ru[q]);
+          } else {
+            finish(a, it, quarter, j, __uint_as_float(rg[q]), __uint_as_float(ru[q]));
           }
+          ++j;
         }
       }
       tc_fence_before();
@@ -398,17 +494,14 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
   }
   __syncwarp();
   if (S > 1) {
-    // at most one unit per cluster: add the S partial sums, the chosen tokens
-    // in turn over the ranks
+    // at most one unit per cluster: add the S partial sums, the tokens in turn
+    // over the ranks
     cluster_sync();
-    if (warp >= 2 && warp < kMma1 && cl < n_units) {
+    if (warp >= 2 && warp < kLoadX && cl < n_units) {
       const int a = cl / NT, it = cl - a * NT, quarter = warp & 3;
-      const unsigned long long mask = s_mask[s_expert[a]];
-      int j = 0;
-      for (int t = 0; t < T; ++t) {
-        if (!((mask >> t) & 1ull)) continue;
-        if (j++ % S != rank) continue;
-        const uint32_t at = base + (t * 128 + quarter * 32 + lane) * 4;
+      const int n = __popcll(ch.mask[a]);
+      for (int j = rank; j < n; j += S) {
+        const uint32_t at = base + (j * 128 + quarter * 32 + lane) * 4;
         float gate[8], up[8];
 #pragma unroll
         for (int p = 0; p < 8; ++p)
@@ -422,7 +515,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
             gate[0] = __fadd_rn(gate[0], gate[p]);
             up[0] = __fadd_rn(up[0], up[p]);
           }
-        finish(a, it, quarter, mask, t, gate[0], up[0]);
+        finish(a, it, quarter, j, gate[0], up[0]);
       }
     }
     cluster_sync();                                       // no CTA leaves while it is read
@@ -444,12 +537,11 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
   using C = Down<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ unsigned long long s_mask[kMoeMaxExperts];  // by active index
-  __shared__ int16_t s_expert[kMoeMaxExperts], s_offset[kMoeMaxExperts];
+  __shared__ Chosen ch;
   __shared__ float s_weight[kMoeMaxTokens * kMoeMaxTopK];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   const uint32_t sums = base + STAGES * C::STAGE_BYTES;   // [BN][128] floats
-  const Bars<STAGES> bars(sums + C::SUM_BYTES);
+  const Bars<STAGES> bars(sums + C::EXTRA_BYTES);
   volatile uint32_t *slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (bars.tmem_slot - raw));
   volatile int *err_ptr = reinterpret_cast<volatile int *>(smem_raw + (bars.err_slot - raw));
@@ -465,17 +557,12 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 32) {
-    bars.init(1);
+    bars.init(2);
     *err_ptr = 0;
   }
   begin_dependent_tma();
-  const int n_active = *tab.n_active;
+  const int n_active = ch.load(tab);
   int rows = 0;                                           // rows of h
-  for (int a = threadIdx.x; a < n_active; a += kThreads) {
-    s_expert[a] = static_cast<int16_t>(tab.expert[a]);
-    s_offset[a] = static_cast<int16_t>(tab.offset[a]);
-    s_mask[a] = tab.mask[a];
-  }
   if (n_active > 0) rows = tab.offset[n_active - 1] + __popcll(tab.mask[n_active - 1]);
   for (int i = threadIdx.x; i < rows; i += kThreads) s_weight[i] = tab.weight[i];
   for (int i = threadIdx.x; i < T * 128; i += kThreads) sum[i] = 0.0f;
@@ -488,15 +575,16 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
   const int lo = static_cast<int>(static_cast<int64_t>(total) * rank / S);
   const int hi = static_cast<int>(static_cast<int64_t>(total) * (rank + 1) / S);
 
-  if (warp == 0) {
+  if (warp == kLoadW || warp == kLoadX) {
+    // one warp loads the weights, the other the rows of h, each with its scales
     Ring<STAGES> ring(1);                                 // the first round finds it empty
     int issued = 0;
     bool ok = true;
     for (int x = lo; x < hi && ok;) {
       const int a = x / KT, k0 = x - a * KT, k1 = min(KT, k0 + hi - x);
-      const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(s_mask[a]) + 15) / 16, 0);
-      const int h0 = __shfl_sync(0xFFFFFFFFu, s_offset[a], 0);
-      const int wt = __shfl_sync(0xFFFFFFFFu, s_expert[a], 0) * NT + nt;   // weight tile
+      const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[a]) + 15) / 16, 0);
+      const int h0 = __shfl_sync(0xFFFFFFFFu, ch.offset[a], 0);
+      const int wt = __shfl_sync(0xFFFFFFFFu, ch.expert[a], 0) * NT + nt;   // weight tile
       const uint8_t *fw = sfw + static_cast<int64_t>(wt) * KT * 512;
       const uint8_t *fh = tab.hsf + static_cast<int64_t>(a) * KT * 512;
       for (int kt = k0; kt < k1; ++kt, ++issued) {
@@ -506,12 +594,16 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
         }
         const uint32_t st = base + ring.s * C::STAGE_BYTES, bar = bars.full + 8 * ring.s;
         if (elect_one()) {
-          mbar_expect_tx(bar, kWTx + nb * 2048 + 2 * 512);
-          tma_load_2d(st, &map_w, kt * 128, wt * 128, bar);
-          for (int i = 0; i < nb; ++i)                    // boxes of 16 rows of h
-            tma_load_2d(st + C::X_OFF + 2048 * i, &map_h, kt * 128, h0 + 16 * i, bar);
-          bulk_load(st + C::SF_OFF, fw + static_cast<int64_t>(kt) * 512, 512, bar);
-          bulk_load(st + C::SF_OFF + 512, fh + static_cast<int64_t>(kt) * 512, 512, bar);
+          if (warp == kLoadW) {
+            mbar_expect_tx(bar, kWTx + 512);
+            tma_load_2d(st, &map_w, kt * 128, wt * 128, bar);
+            bulk_load(st + C::SF_OFF, fw + static_cast<int64_t>(kt) * 512, 512, bar);
+          } else {
+            mbar_expect_tx(bar, nb * 2048 + 512);
+            for (int i = 0; i < nb; ++i)                  // boxes of 16 rows of h
+              tma_load_2d(st + C::X_OFF + 2048 * i, &map_h, kt * 128, h0 + 16 * i, bar);
+            bulk_load(st + C::SF_OFF + 512, fh + static_cast<int64_t>(kt) * 512, 512, bar);
+          }
         }
         __syncwarp();
         ring.next();
@@ -523,26 +615,23 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       *err_ptr = 1;
       drain_loads<STAGES>(bars.full, issued);
     }
-  } else if (warp == kMma0 || warp == kMma1) {
-    // the K-tiles of an expert in turn, each warp into an accumulator of its own
-    const int w = warp == kMma1;
+  } else if (warp == kMma) {
     Ring<STAGES> ring(0);
-    int b = 0;                                            // accumulators and their phase
+    int b = 0;                                            // accumulator and its phase
     uint32_t bphase = 1;
     bool ok = true;
     const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
     const uint64_t dsf = desc_sf(base + C::SF_OFF);
     for (int x = lo; x < hi && ok;) {
-      const int a = x / KT, k0 = x - a * KT, n = min(KT - k0, hi - x);
-      const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(s_mask[a]) + 15) / 16, 0);
+      const int a = x / KT, k0 = x - a * KT, k1 = min(KT, k0 + hi - x);
+      const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[a]) + 15) / 16, 0);
       const uint32_t idesc = idesc_mx4x8(16 * nb);
       if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      for (int i = 0; i < n; ++i, ring.next()) {
-        if ((i & 1) != w) continue;
+      for (int kt = k0; kt < k1; ++kt) {
         if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
           ok = false;
           break;
@@ -551,25 +640,24 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
         const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s;
         const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
         if (elect_one()) {
-          mma_ktile_mx4x8<1>(tmem + (2 * b + w) * BN, dw + at, dx + at, dsf + at, dsf + at + 32,
-                             sf, sf + 4, 0, idesc, i >= 2);
+          mma_ktile_mx4x8<1>(tmem + b * BN, dw + at, dx + at, dsf + at, dsf + at + 32, sf, sf + 4,
+                             0, idesc, kt != k0);
           tc_commit(bars.empty + 8 * ring.s);
-          if (i + 2 >= n) tc_commit(bars.acc_full + 8 * b);
+          if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
         }
         __syncwarp();
+        ring.next();
       }
-      if (w == 1 && n == 1 && lane == 0) mbar_arrive(bars.acc_full + 8 * b);   // nothing to add
-      __syncwarp();
-      x += n;
+      x += k1 - k0;
       b ^= 1;
       if (b == 0) bphase ^= 1;
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
     if (!ok) {                                            // wait for the MMAs in flight
       *err_ptr = 1;
-      if (elect_one()) tc_commit(bars.drain + 8 * w);
+      if (elect_one()) tc_commit(bars.drain);
       __syncwarp();
-      warp_wait(bars.drain + 8 * w, 0);
+      warp_wait(bars.drain, 0);
     }
   } else if (lo < hi) {
     const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -581,21 +669,14 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
         break;
       }
       tc_fence_after();
-      unsigned long long mask = s_mask[a];
-      const float *w = s_weight + s_offset[a];
-      const uint32_t acc = tmem + 2 * b * BN + (static_cast<uint32_t>(quarter * 32) << 16);
-      // one K-tile alone is all in the first accumulator
-      const bool two = min((a + 1) * KT, hi) - max(a * KT, lo) > 1;
+      unsigned long long mask = ch.mask[a];
+      const float *w = s_weight + ch.offset[a];
+      const uint32_t acc = tmem + b * BN + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
       for (int j = 0; mask != 0; j += 16) {
-        uint32_t r[16], r1[16];
+        uint32_t r[16];
         tc_load16(acc + j, r);
-        tc_load16(acc + BN + j, r1);
         tc_wait_ld();
-        if (two)
-#pragma unroll
-          for (int q = 0; q < 16; ++q)
-            r[q] = __float_as_uint(__fadd_rn(__uint_as_float(r[q]), __uint_as_float(r1[q])));
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
           if (mask == 0) continue;
@@ -623,15 +704,17 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
 }
 
 struct Layout {
-  size_t expert, offset, mask, weight, hq, hsf, bytes;
-  Layout(int64_t T, int64_t E, int64_t k, int64_t I) {
+  size_t expert, offset, mask, weight, xq, xsf, hq, hsf, bytes;
+  Layout(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
     const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t most = static_cast<size_t>(T * k < E ? T * k : E);   // chosen experts at most
     expert = 256;
     offset = expert + up(4 * most);
     mask = offset + up(4 * most);
     weight = mask + up(8 * most);
-    hq = weight + up(4 * T * k);
+    xq = weight + up(4 * T * k);
+    xsf = xq + (T > 16 ? up(T * k * H) : 0);
+    hq = xsf + (T > 16 ? most * (H / 128) * 512 : 0);
     hsf = hq + up(T * k * I);
     bytes = hsf + most * (I / 128) * 512;
   }
@@ -641,7 +724,8 @@ template <typename OutT, int BN>
 cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   static KernelSetup setup1, setup2;
   int per_sm = 0;
-  auto *k1 = gate_up_kernel<BN>;
+  constexpr bool kSorted = BN > 16;
+  auto *k1 = gate_up_kernel<BN, kSorted>;
   auto *k2 = down_kernel<OutT, BN>;
   cudaError_t e = kernel_setup(setup1, reinterpret_cast<const void *>(k1), kThreads,
                                GateUp<BN>::SMEM_BYTES, &per_sm);
@@ -652,20 +736,29 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   const int KT1 = static_cast<int>(m.H / 128), NT1 = static_cast<int>(m.I / 128);
   CUtensorMap w13, w2, x, h;
   if (!make_map_mxfp4(&w13, m.w13, m.E * 2 * m.I, m.H) ||
-      !make_map_mxfp4(&w2, m.w2, m.E * m.H, m.I) || !make_map_mxfp8(&x, m.xq, m.T, m.H, BN) ||
+      !make_map_mxfp4(&w2, m.w2, m.E * m.H, m.I) || 
+      !make_map_mxfp8(&x, kSorted ? tab.xq : m.xq, kSorted ? m.T * m.k : m.T, m.H, 16) ||
       !make_map_mxfp8(&h, tab.hq, m.T * m.k, m.I, 16))
     return cudaErrorInvalidValue;
+  if (kSorted) {
+    e = launch_dependent(route_kernel, m.T * m.k < 128 ? m.T * m.k : 128, kRouteThreads, 0, 1, L,
+                         m.xq, m.xsf, m.logits, m.logits_dtype, m.T, m.E, m.k, m.renormalize,
+                         KT1, tab);
+    if (e != cudaSuccess) return e;
+  }
   // first product: (chosen expert, tile of h) units over persistent CTAs, or
   // one cluster each where even the most units leave SMs idle
   const int64_t most = (m.T * m.k < m.E ? m.T * m.k : m.E) * NT1;
+  int64_t slots = static_cast<int64_t>(L.num_sms) * GateUp<BN>::PER_SM;
   int S = 1;
-  while (S < 8 && most * S * 2 <= L.num_sms && KT1 >= 4 * S) S *= 2;
-  e = launch_dependent(k1, S > 1 ? most * S : most < L.num_sms ? most : L.num_sms, kThreads,
+  while (S < 8 && most * S * 2 <= slots && KT1 >= 2 * S) S *= 2;
+  e = launch_dependent(k1, S > 1 ? most * S : most < slots ? most : slots, kThreads,
                        GateUp<BN>::SMEM_BYTES, S, L, w13, x, m.sf13, m.xsf, m.logits,
                        m.logits_dtype, m.T, m.E, m.k, m.renormalize, KT1, NT1, S, tab, m.status);
   if (e != cudaSuccess) return e;
   // second product: the largest cluster that leaves every cluster its place
-  const int64_t tiles = m.H / 128, slots = static_cast<int64_t>(L.num_sms) * Down<BN>::PER_SM;
+  const int64_t tiles = m.H / 128;
+  slots = static_cast<int64_t>(L.num_sms) * Down<BN>::PER_SM;
   S = 1;
   while (S < 8 && tiles * S * 2 <= slots) S *= 2;
   return launch_dependent(k2, tiles * S, kThreads, Down<BN>::SMEM_BYTES, S, L, w2, h, m.sf2, tab,
@@ -674,12 +767,12 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
 
 }  // namespace
 
-size_t moe_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t I) {
-  return Layout(T, E, k, I).bytes;
+size_t moe_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I) {
+  return Layout(T, E, k, H, I).bytes;
 }
 
 cudaError_t launch_moe_mxfp4(const MoeArgs &m, void *workspace, const Launch &L) {
-  const Layout at(m.T, m.E, m.k, m.I);
+  const Layout at(m.T, m.E, m.k, m.H, m.I);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   Table tab;
   tab.n_active = reinterpret_cast<int *>(ws);
@@ -687,6 +780,8 @@ cudaError_t launch_moe_mxfp4(const MoeArgs &m, void *workspace, const Launch &L)
   tab.offset = reinterpret_cast<int *>(ws + at.offset);
   tab.mask = reinterpret_cast<unsigned long long *>(ws + at.mask);
   tab.weight = reinterpret_cast<float *>(ws + at.weight);
+  tab.xq = ws + at.xq;
+  tab.xsf = ws + at.xsf;
   tab.hq = ws + at.hq;
   tab.hsf = ws + at.hsf;
   auto go = [&](auto o) {
