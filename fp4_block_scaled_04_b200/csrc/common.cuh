@@ -528,6 +528,11 @@ __device__ __forceinline__ U32x4 philox(const PhiloxKey &K, uint32_t c0, uint32_
 // cp.async staging (16-byte global -> shared copies, grouped per thread)
 // ---------------------------------------------------------------------------
 
+// shared-memory address of a generic pointer
+__device__ __forceinline__ uint32_t smem_u32(const void *p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }

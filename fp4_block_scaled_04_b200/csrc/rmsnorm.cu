@@ -19,7 +19,9 @@
 namespace fp4q {
 namespace {
 
-// 8 consecutive elements as they lie in memory
+// 8 consecutive elements as they lie in memory, and as four pairs of floats (the
+// arithmetic below runs on f32x2 pairs: at one value an instruction these kernels
+// are bound by issue and not by HBM).
 template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> {
   uint4 a;
@@ -29,18 +31,28 @@ template <> struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void store(__nv_bfloat16 *p) const {
     *reinterpret_cast<uint4 *>(p) = a;
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
-    v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(bf16_lo(a.x), bf16_hi(a.x));
+    v[1] = make_float2(bf16_lo(a.y), bf16_hi(a.y));
+    v[2] = make_float2(bf16_lo(a.z), bf16_hi(a.z));
+    v[3] = make_float2(bf16_lo(a.w), bf16_hi(a.w));
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
+  __device__ __forceinline__ void set(const float2 (&v)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
       memcpy(&w[i], &h, sizeof(uint32_t));
     }
     a = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // this + o, rounded once (as the FP32 sum rounded to BF16: where that sum is
+  // inexact, it lies nowhere near the middle of two BF16 values)
+  __device__ __forceinline__ void add(const Raw8 &o) {
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(a.x) : "r"(o.a.x));
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(a.y) : "r"(o.a.y));
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(a.z) : "r"(o.a.z));
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(a.w) : "r"(o.a.w));
   }
 };
 template <> struct Raw8<float> {
@@ -53,20 +65,64 @@ template <> struct Raw8<float> {
     reinterpret_cast<float4 *>(p)[0] = a;
     reinterpret_cast<float4 *>(p)[1] = b;
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ void get(float2 (&v)[4]) const {
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
   }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
-    a = make_float4(v[0], v[1], v[2], v[3]);
-    b = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ __forceinline__ void set(const float2 (&v)[4]) {
+    a = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    b = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+  }
+  __device__ __forceinline__ void add(const Raw8 &o) {
+    float2 v[4], w[4];
+    get(v);
+    o.get(w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], w[i]);
+    set(v);
   }
 };
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A ring of rows in shared memory, filled by cp.async.  A thread copies the
+// vectors that it reads itself, so that it needs no barrier, only its own
+// groups' completion.  A row's 16-byte pieces lie plane by plane (an FP32 vector
+// of 8 values has two), so that neighbouring lanes use neighbouring banks.
+template <typename T>
+__device__ __forceinline__ void ring_copy(uint32_t row, const T *p, int v8, int n8) {
+#pragma unroll
+  for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+    cp_async16(row + (h * n8 + v8) * 16, reinterpret_cast<const uint8_t *>(p) + 16 * h);
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> ring_get(const uint8_t *row, int v8, int n8) {
+  Raw8<T> r;
+#pragma unroll
+  for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
+    reinterpret_cast<uint4 *>(&r)[h] = *reinterpret_cast<const uint4 *>(row + (h * n8 + v8) * 16);
+  return r;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
+}
+
+// 1 / sqrt(v): the hardware's estimate and one Newton step (every thread works a
+// row's out, and the correctly rounded operations took a third of the row's time)
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  const float e = __fmaf_rn(-__fmul_rn(v, r), r, 1.0f);
+  return v > 0.0f ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
+}
+
+// max(m, |a|, |b|)
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+  return fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
 }
 
 // The sum of one value per thread over the W warps of a row, in an order that
@@ -81,97 +137,174 @@ __device__ __forceinline__ float row_sum(float v, float *slot, int warp) {
   __syncthreads();
   const float *mine = slot + warp / W * W;
   float t = 0.0f;
+  if constexpr (W == 2) {
+    t = mine[0] + mine[1];
+  } else {
 #pragma unroll
-  for (int i = 0; i < W; ++i) t += mine[i];
+    for (int i = 0; i < W / 4; ++i) {
+      const float4 f = reinterpret_cast<const float4 *>(mine)[i];
+      t += (f.x + f.y) + (f.z + f.w);
+    }
+  }
   return t;
 }
 
-// W warps share a row; a CTA holds max(W, 4) warps.  A thread keeps up to VPT
-// vectors of 8 values in registers: vector lane + 32 (warp in row) + 32 W j,
-// so a warp's loads are contiguous and the 4 lanes of a 32-value block are
-// neighbours.  One read of x and r, one write of everything else.
-template <typename T, typename TW, int W, int VPT>
-__global__ void __launch_bounds__((W < 4 ? 4 : W) * 32)
+// W warps share a row; a CTA holds max(W, 4) warps, so G = 1, 2 or 4 rows at a
+// time, and walks the groups of rows blockIdx.x, + gridDim.x, ...  A thread keeps
+// up to VPT vectors of 8 values in registers: vector lane + 32 (warp in row) +
+// 32 W j, so a warp's loads are contiguous and the 4 lanes of a 32-value block are
+// neighbours.  DEPTH > 0: a ring of DEPTH groups in shared memory keeps loads in
+// flight through the reduction and the stores (8192 x 4096 BF16 with a residual:
+// 39 us, 5.99 TB/s; 53 without it).  Rows too wide for it are loaded directly
+// (DEPTH 0).
+template <typename T, typename TW, int W, int VPT, int DEPTH, bool FULL>
+__global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
 rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int64_t ld_res,
                const TW *__restrict__ weight, float eps, int mode, uint8_t *__restrict__ q,
                uint8_t *__restrict__ sf, int scale_layout, float *__restrict__ rstd_out,
                T *sum_out, T *__restrict__ y_out) {
-  constexpr int NW = W < 4 ? 4 : W;
-  __shared__ float slot[NW];
+  constexpr int NW = W < 4 ? 4 : W, G = NW / W;
+  extern __shared__ __align__(16) uint8_t ring[];        // [DEPTH][x, residual][G] rows
+  __shared__ __align__(16) float slot[2][NW];
   begin_dependent();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (NW / W) + warp / W;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
   const int n8 = cols / 8, bpr = cols / 32;
+  const int row_bytes = cols * static_cast<int>(sizeof(T)), tensors = res ? 2 : 1;
   const int64_t srows = scale_rows(rows, scale_layout);
   const int64_t scols = scale_cols(bpr, scale_layout);
-  const bool live = row < rows;
-  Raw8<T> s[VPT];
-  float ss = 0.0f;
+  const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(cols));
+  // FULL: every thread has all its vectors (cols == 256 W VPT)
+  auto mine = [&](int v8) { return FULL || v8 < n8; };
+  // a scale byte's offset: the row's part and the column's
+  auto sf_row = [&](int64_t r) {
+    return scale_layout == FP4Q_SCALE_LINEAR
+               ? r * scols
+               : (r >> 7) * (scols >> 2) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+  };
+  auto sf_col = [&](int c) {
+    return scale_layout == FP4Q_SCALE_LINEAR ? c : (c >> 2) * 512 + (c & 3);
+  };
+  const bool padded = scols != bpr || srows != rows;
+  // four scale bytes at a time where their addresses allow it
+  const bool words = scols % 4 == 0 && reinterpret_cast<uintptr_t>(sf) % 4 == 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  auto place = [&](int stage, int t) { return ((stage * tensors + t) * G + grp) * row_bytes; };
+  auto fetch = [&](int stage, int64_t row) {
+    if (row < rows) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v8 = lane + 32 * (wr + W * j);
+        if (mine(v8)) {
+          ring_copy(smem_u32(ring) + place(stage, 0), x + row * ld + 8 * v8, v8, n8);
+          if (res)
+            ring_copy(smem_u32(ring) + place(stage, 1), res + row * ld_res + 8 * v8, v8, n8);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + grp;
+  if constexpr (DEPTH > 0)
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d) fetch(d, row + d * step);
+  Raw8<TW> wv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v8 = lane + 32 * (wr + W * j);
-    if (live && v8 < n8) {
-      s[j].load(x + row * ld + 8 * v8);
-      float v[8];
-      if (res) {
+    if (mine(v8)) wv[j].load(weight + 8 * v8);
+  }
+  int stage = 0, turn = 0;
+  // every group of the CTA makes the same number of steps (row_sum has CTA
+  // barriers)
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < srows;
+       row0 += step, row += step, turn ^= 1) {
+    const bool live = row < rows;
+    const int64_t e0 = row * cols;
+    uint8_t *const sf_at = sf + sf_row(row);
+    if constexpr (DEPTH > 0) {
+      fetch(stage == 0 ? DEPTH - 1 : stage - 1, row + (DEPTH - 1) * step);
+      cp_async_wait<DEPTH - 1>();
+    }
+    Raw8<T> s[VPT];
+    float2 ss = both(0.0f);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v8 = lane + 32 * (wr + W * j);
+      if (live && mine(v8)) {
         Raw8<T> rr;
-        rr.load(res + row * ld_res + 8 * v8);
-        float a[8], b[8];
-        s[j].get(a);
-        rr.get(b);
+        if constexpr (DEPTH > 0) {
+          s[j] = ring_get<T>(ring + place(stage, 0), v8, n8);
+          if (res) rr = ring_get<T>(ring + place(stage, 1), v8, n8);
+        } else {
+          s[j].load(x + row * ld + 8 * v8);
+          if (res) rr.load(res + row * ld_res + 8 * v8);
+        }
+        if (res) s[j].add(rr);
+        float2 v[4];
+        s[j].get(v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __fadd_rn(a[k], b[k]);
-        s[j].set(v);
-      }
-      s[j].get(v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = __fmaf_rn(v[k], v[k], ss);
-    }
-  }
-  const float total = row_sum<W>(ss, slot, warp);
-  const float rstd = __fdiv_rn(
-      1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(total, static_cast<float>(cols)), eps)));
-  if (live && rstd_out && wr == 0 && lane == 0) rstd_out[row] = rstd;
-#pragma unroll
-  for (int j = 0; j < VPT; ++j) {
-    const int v8 = lane + 32 * (wr + W * j);
-    const bool on = live && v8 < n8;
-    float v[8];
-    float m = 0.0f;
-    if (on) {
-      if (sum_out) s[j].store(sum_out + row * cols + 8 * v8);
-      Raw8<TW> wv;
-      wv.load(weight + 8 * v8);
-      float w[8];
-      s[j].get(v);
-      wv.get(w);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] = __fmul_rn(__fmul_rn(v[k], rstd), w[k]);
-        m = fmaxf(m, fabsf(v[k]));
-      }
-      if (y_out) {
-        Raw8<T> o;
-        o.set(v);
-        o.store(y_out + row * cols + 8 * v8);
+        for (int k = 0; k < 4; ++k) ss = fma2(v[k], v[k], ss);
       }
     }
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    if (on) {
-      const uint32_t byte = e8m0_biased_e4m3(m, mode);
-      *reinterpret_cast<uint2 *>(q + row * cols + 8 * v8) = e4m3x8_scaled(v, e8m0_inverse(byte));
-      if ((lane & 3) == 0)
-        sf[scale_offset(row, v8 / 4, scols, scale_layout)] = static_cast<uint8_t>(byte);
+    const float total = row_sum<W>(__fadd_rn(ss.x, ss.y), slot[turn], warp);
+    const float rstd = inv_sqrt(__fmaf_rn(total, inv_cols, eps));
+    if (live && rstd_out && wr == 0 && lane == 0) rstd_out[row] = rstd;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int v8 = lane + 32 * (wr + W * j);
+      const bool on = live && mine(v8);
+      float2 v[4];
+      float m = 0.0f;
+      if (on) {
+        if (sum_out) s[j].store(sum_out + e0 + 8 * v8);
+        float2 w[4];
+        s[j].get(v);
+        wv[j].get(w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[k] = mul2(mul2(v[k], both(rstd)), w[k]);
+          m = max_abs3(m, v[k].x, v[k].y);
+        }
+        if (y_out) {
+          Raw8<T> o;
+          o.set(v);
+          o.store(y_out + e0 + 8 * v8);
+        }
+      }
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const uint32_t byte = e8m0_biased_e4m3(m, mode);   // 0 past the row's end
+      if (on) {
+        const float2 inv = both(e8m0_inverse(byte));
+        *reinterpret_cast<uint2 *>(q + e0 + 8 * v8) =
+            make_uint2(e4m3x4(mul2(v[0], inv), mul2(v[1], inv)),
+                       e4m3x4(mul2(v[2], inv), mul2(v[3], inv)));
+      }
+      if (words) {                                       // lanes 0 and 16: 4 blocks each
+        const uint32_t two = byte | __shfl_down_sync(0xFFFFFFFFu, byte, 4) << 8;
+        const uint32_t four = two | __shfl_down_sync(0xFFFFFFFFu, two, 8) << 16;
+        if (on && (lane & 15) == 0)
+          *reinterpret_cast<uint32_t *>(sf_at + sf_col(v8 / 4)) = four;
+      } else if (on && (lane & 3) == 0) {
+        sf_at[sf_col(v8 / 4)] = static_cast<uint8_t>(byte);
+      }
     }
+    // the swizzled layout's padding: whole rows past the matrix, and the scale
+    // columns past cols / 32
+    if (padded && row < srows) {
+      const int64_t c0 = live ? bpr : 0;
+      for (int64_t c = c0 + wr * 32 + lane; c < scols; c += W * 32)
+        sf_at[sf_col(static_cast<int>(c))] = 0;
+    }
+    if (++stage == DEPTH) stage = 0;
   }
-  // the swizzled layout's padding: whole rows past the matrix, and the scale
-  // columns past cols / 32
-  if (row < srows) {
-    const int64_t c0 = live ? bpr : 0;
-    for (int64_t c = c0 + wr * 32 + lane; c < scols; c += W * 32)
-      sf[scale_offset(row, c, scols, scale_layout)] = 0;
-  }
+  cp_async_wait<0>();
+}
+
+// The depth of the ring: 3 groups of rows of `bytes` each, where they fit next to
+// `fixed` bytes, else none.
+inline int ring_depth(int64_t bytes, int64_t fixed) {
+  return 3 * bytes + fixed <= 220 * 1024 ? 3 : 0;
 }
 
 template <typename T, typename TW>
@@ -180,175 +313,249 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
                        uint8_t *sf, int layout, float *rstd, void *sum, void *y,
                        const Launch &L) {
   const int64_t n8 = cols / 8, srows = scale_rows(rows, layout);
-  auto go = [&](auto w, auto v) {
-    constexpr int W = decltype(w)::value, VPT = decltype(v)::value, NW = W < 4 ? 4 : W;
-    const int64_t grid = (srows + NW / W - 1) / (NW / W);
-    return launch_dependent(rmsnorm_kernel<T, TW, W, VPT>, grid, NW * 32, 0, 1, L,
-                            static_cast<const T *>(x), rows, static_cast<int>(cols), ld,
-                            static_cast<const T *>(res), ld_res, static_cast<const TW *>(weight),
-                            eps, mode, q, sf, layout, rstd, static_cast<T *>(sum),
-                            static_cast<T *>(y));
+  auto run = [&](auto w, auto v, auto d, auto full) {
+    constexpr int W = decltype(w)::value, VPT = decltype(v)::value, D = decltype(d)::value;
+    constexpr int NW = W < 4 ? 4 : W, G = NW / W;
+    auto *kern = rmsnorm_kernel<T, TW, W, VPT, D, decltype(full)::value>;
+    const int smem = static_cast<int>(D * (res ? 2 : 1) * G * cols * sizeof(T));
+    static KernelSetup setup;
+    int per_sm = 0;
+    cudaError_t e = kernel_setup(setup, reinterpret_cast<const void *>(kern), NW * 32,
+                                 D ? 220 * 1024 : 0, &per_sm);
+    if (e != cudaSuccess) return e;
+    const int64_t steps = (srows + G - 1) / G;
+    int64_t grid = steps;                                // without a ring a row's CTA ends
+    if (D > 0) {
+      int64_t fit = (228 * 1024) / (smem + 1024 + 512);
+      const int64_t threads = NW <= 16 ? 512 / (NW * 32) : 1;   // of 128 registers
+      if (fit > threads) fit = threads;
+      if (grid > fit * L.num_sms) grid = fit * L.num_sms;
+    }
+    return launch_dependent(kern, grid, NW * 32, smem, 1, L, static_cast<const T *>(x), rows,
+                            static_cast<int>(cols), ld, static_cast<const T *>(res), ld_res,
+                            static_cast<const TW *>(weight), eps, mode, q, sf, layout, rstd,
+                            static_cast<T *>(sum), static_cast<T *>(y));
   };
+  using std::false_type;
   using std::integral_constant;
-  // the fewest warps that hold the row in two vectors a thread; rows beyond
-  // 32 warps take four
-  if (n8 <= 64) return go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (n8 <= 128) return go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-  if (n8 <= 256) return go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (n8 <= 512) return go(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  if (n8 <= 1024) return go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  if (n8 <= 2048) return go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  return go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  auto go = [&](auto w) {
+    constexpr int W = decltype(w)::value, G = W < 4 ? 4 / W : 1;
+    constexpr integral_constant<int, 4> vpt{};
+    if (ring_depth((res ? 2 : 1) * G * cols * static_cast<int64_t>(sizeof(T)), 0) == 0)
+      return run(w, vpt, integral_constant<int, 0>{}, false_type{});
+    if (cols == 256 * W * 4) return run(w, vpt, integral_constant<int, 3>{}, std::true_type{});
+    return run(w, vpt, integral_constant<int, 3>{}, false_type{});
+  };
+  // Few rows: each on as many warps as it has vectors, no ring.  Many: the fewest
+  // warps that hold a row in four vectors a thread, which spread the work that
+  // each row costs once over the most values (8192 x 4096 BF16: 39.4 us on four
+  // warps, 41.7 on eight, 55 on two).
+  if (rows <= L.num_sms && n8 <= 1024) {
+    constexpr integral_constant<int, 1> one{};
+    constexpr integral_constant<int, 0> none{};
+    if (n8 <= 32) return run(integral_constant<int, 1>{}, one, none, false_type{});
+    if (n8 <= 128) return run(integral_constant<int, 4>{}, one, none, false_type{});
+    if (n8 <= 512) return run(integral_constant<int, 16>{}, one, none, false_type{});
+    return run(integral_constant<int, 32>{}, one, none, false_type{});
+  }
+  if (n8 <= 128) return go(integral_constant<int, 1>{});
+  if (n8 <= 256) return go(integral_constant<int, 2>{});
+  if (n8 <= 512) return go(integral_constant<int, 4>{});
+  if (n8 <= 1024) return go(integral_constant<int, 8>{});
+  if (n8 <= 2048) return go(integral_constant<int, 16>{});
+  return go(integral_constant<int, 32>{});
 }
 
-// Backward: a CTA walks the rows blockIdx.x, + gridDim.x, ... and keeps its
-// part of dw in shared memory (every thread owns its columns, so the sums
-// need no atomics and their order depends on the grid alone); the parts are
-// added up by dweight_kernel.  W and VPT as in the forward kernel, one row
-// per CTA and step for W >= 4, 4 / W rows with a dw part each below that.
-template <typename T, typename TW, int W, int VPT>
-__global__ void __launch_bounds__((W < 4 ? 4 : W) * 32)
-rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s,
-                        int64_t ld_s, const TW *__restrict__ weight,
-                        const float *__restrict__ rstd, const T *dsum,
-                        int64_t ld_dsum, int64_t rows, int cols, T *dx,
+// Backward: a CTA walks the groups of rows as above and keeps its part of dw in
+// shared memory (every thread owns its columns, so the sums need no atomics and
+// their order depends on the grid alone); the parts are added up by
+// dweight_kernel.  Rows come through the ring where it fits (8192 x 4096 BF16 with
+// dsum: 45.5 us with dweight_kernel, 5.9 TB/s; 49-60 in direct forms, which
+// alternate between loading and computing).
+template <typename T, typename TW, int W, int VPT, int DEPTH>
+__global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
+rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s, int64_t ld_s,
+                        const TW *__restrict__ weight, const float *__restrict__ rstd,
+                        const T *dsum, int64_t ld_dsum, int64_t rows, int cols, T *dx,
                         float *__restrict__ part) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
-  extern __shared__ float dw[];                          // [G][cols]
-  __shared__ float slot[2][NW];
+  extern __shared__ __align__(16) uint8_t ring[];        // [DEPTH][dy, s, dsum][G] rows, [G] dw
+  __shared__ __align__(16) float slot[2][NW];
   begin_dependent();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
   const int n8 = cols / 8;
-  float *mine = dw + grp * cols;
+  const int row_bytes = cols * static_cast<int>(sizeof(T)), tensors = dsum ? 3 : 2;
+  float *dw = reinterpret_cast<float *>(ring + static_cast<size_t>(DEPTH) * tensors * G * row_bytes);
+  // this row's part, in two planes of float4 as the ring's
+  uint8_t *mine = reinterpret_cast<uint8_t *>(dw + grp * cols);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
     const int v8 = lane + 32 * (wr + W * j);
-    if (v8 < n8) {
-      reinterpret_cast<float4 *>(mine)[2 * v8] = make_float4(0, 0, 0, 0);
-      reinterpret_cast<float4 *>(mine)[2 * v8 + 1] = make_float4(0, 0, 0, 0);
-    }
+    if (v8 < n8)
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float4 *>(mine + (h * n8 + v8) * 16) = make_float4(0, 0, 0, 0);
   }
   const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(cols));
-  int turn = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  auto place = [&](int stage, int t) { return ((stage * tensors + t) * G + grp) * row_bytes; };
+  auto fetch = [&](int stage, int64_t row) {
+    if (row < rows) {
+#pragma unroll
+      for (int j = 0; j < VPT; ++j) {
+        const int v8 = lane + 32 * (wr + W * j);
+        if (v8 < n8) {
+          ring_copy(smem_u32(ring) + place(stage, 0), dy + row * ld_dy + 8 * v8, v8, n8);
+          ring_copy(smem_u32(ring) + place(stage, 1), s + row * ld_s + 8 * v8, v8, n8);
+          if (dsum)
+            ring_copy(smem_u32(ring) + place(stage, 2), dsum + row * ld_dsum + 8 * v8, v8, n8);
+        }
+      }
+    }
+    cp_async_commit();
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + grp;
+  if constexpr (DEPTH > 0)
+#pragma unroll
+    for (int d = 0; d < DEPTH - 1; ++d) fetch(d, row + d * step);
+  Raw8<TW> wv[VPT];
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int v8 = lane + 32 * (wr + W * j);
+    if (v8 < n8) wv[j].load(weight + 8 * v8);
+  }
+  int stage = 0, turn = 0;
   // every group of the CTA makes the same number of steps (row_sum has CTA
   // barriers)
   for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * G; row0 < rows;
-       row0 += static_cast<int64_t>(gridDim.x) * G, turn ^= 1) {
-    const int64_t row = row0 + grp;
+       row0 += step, row += step, turn ^= 1) {
     const bool live = row < rows;
-    const float r = live ? __ldg(rstd + row) : 0.0f;
+    const float r = live ? rstd[row] : 0.0f;
+    if constexpr (DEPTH > 0) {
+      fetch(stage == 0 ? DEPTH - 1 : stage - 1, row + (DEPTH - 1) * step);
+      cp_async_wait<DEPTH - 1>();
+    }
     Raw8<T> gv[VPT], sv[VPT], dv[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v8 = lane + 32 * (wr + W * j);
       if (live && v8 < n8) {
-        gv[j].load(dy + row * ld_dy + 8 * v8);
-        sv[j].load(s + row * ld_s + 8 * v8);
-        if (dsum) dv[j].load(dsum + row * ld_dsum + 8 * v8);
+        if constexpr (DEPTH > 0) {
+          gv[j] = ring_get<T>(ring + place(stage, 0), v8, n8);
+          sv[j] = ring_get<T>(ring + place(stage, 1), v8, n8);
+          if (dsum) dv[j] = ring_get<T>(ring + place(stage, 2), v8, n8);
+        } else {
+          gv[j].load(dy + row * ld_dy + 8 * v8);
+          sv[j].load(s + row * ld_s + 8 * v8);
+          if (dsum) dv[j].load(dsum + row * ld_dsum + 8 * v8);
+        }
       }
     }
-    float dot = 0.0f;
+    float2 dot = both(0.0f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v8 = lane + 32 * (wr + W * j);
       if (live && v8 < n8) {
-        float g[8], x[8], w[8], acc[8];
-        Raw8<TW> wv;
-        wv.load(weight + 8 * v8);
+        float2 g[4], x[4], w[4], acc[4];
         gv[j].get(g);
         sv[j].get(x);
-        wv.get(w);
-        Raw8<float> a;
-        a.load(mine + 8 * v8);
+        wv[j].get(w);
+        Raw8<float> a = ring_get<float>(mine, v8, n8);
         a.get(acc);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float xh = __fmul_rn(x[k], r);
-          dot = __fmaf_rn(__fmul_rn(g[k], w[k]), xh, dot);
-          acc[k] = __fmaf_rn(g[k], xh, acc[k]);
+        for (int k = 0; k < 4; ++k) {
+          const float2 xh = mul2(x[k], both(r));
+          dot = fma2(mul2(g[k], w[k]), xh, dot);
+          acc[k] = fma2(g[k], xh, acc[k]);
         }
         a.set(acc);
-        a.store(mine + 8 * v8);
+        *reinterpret_cast<float4 *>(mine + v8 * 16) = a.a;
+        *reinterpret_cast<float4 *>(mine + (n8 + v8) * 16) = a.b;
       }
     }
-    const float c = __fmul_rn(row_sum<W>(dot, slot[turn], warp), inv_cols);
+    const float c = __fmul_rn(row_sum<W>(__fadd_rn(dot.x, dot.y), slot[turn], warp), inv_cols);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v8 = lane + 32 * (wr + W * j);
       if (live && v8 < n8) {
-        float g[8], x[8], w[8], o[8];
-        Raw8<TW> wv;
-        wv.load(weight + 8 * v8);
+        float2 g[4], x[4], w[4];
         gv[j].get(g);
         sv[j].get(x);
-        wv.get(w);
+        wv[j].get(w);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float xh = __fmul_rn(x[k], r);
-          o[k] = __fmul_rn(r, __fmaf_rn(-xh, c, __fmul_rn(g[k], w[k])));
-        }
+        for (int k = 0; k < 4; ++k)
+          g[k] = mul2(both(r), fma2(mul2(x[k], both(r)), both(-c), mul2(g[k], w[k])));
         if (dsum) {
-          float d[8];
+          float2 d[4];
           dv[j].get(d);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) o[k] = __fadd_rn(o[k], d[k]);
+          for (int k = 0; k < 4; ++k) g[k] = add2(g[k], d[k]);
         }
         Raw8<T> out;
-        out.set(o);
+        out.set(g);
         out.store(dx + row * cols + 8 * v8);
       }
     }
+    if (++stage == DEPTH) stage = 0;
   }
+  cp_async_wait<0>();
   __syncthreads();
+  // column 8 v8 + 4 h + i lies in plane h
   for (int i = threadIdx.x; i < cols; i += NW * 32) {
-    float t = dw[i];
+    const int at = ((i / 4 % 2) * n8 + i / 8) * 4 + i % 4;
+    float t = dw[at];
 #pragma unroll
-    for (int g = 1; g < G; ++g) t += dw[g * cols + i];
+    for (int g = 1; g < G; ++g) t += dw[g * cols + at];
     part[static_cast<int64_t>(blockIdx.x) * cols + i] = t;
   }
 }
 
-// dw[c] = sum of part[p][c] over p, 8 strands per column, then in order
-__global__ void __launch_bounds__(256)
-dweight_kernel(const float *__restrict__ part, int parts, int cols, float *__restrict__ dweight) {
-  __shared__ float t[8][32];
+// dw[c] = sum of part[p][c] over p, 32 strands per column, then in order
+__global__ void __launch_bounds__(1024)
+dweight_kernel(const float *part, int parts, int cols, float *dweight) {
+  __shared__ float t[32][33];
   const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;                  // cols % 32 == 0
   begin_dependent();
   float a = 0.0f;
-  for (int p = strand; p < parts; p += 8) a += part[static_cast<int64_t>(p) * cols + c];
+#pragma unroll 8
+  for (int p = strand; p < parts; p += 32) a += part[static_cast<int64_t>(p) * cols + c];
   t[strand][lane] = a;
   __syncthreads();
   if (strand == 0) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) a += t[i][lane];
+    for (int i = 1; i < 32; ++i) a += t[i][lane];
     dweight[c] = a;
   }
 }
 
-template <typename T, typename TW, int W, int VPT>
+template <typename T, typename TW, int W, int VPT, int D>
 cudaError_t launch_bwd_t(const void *dy, int64_t ld_dy, const void *s, int64_t ld_s,
                          const void *weight, const float *rstd, const void *dsum,
                          int64_t ld_dsum, int64_t rows, int64_t cols, void *dx, float *dweight,
                          float *part, const Launch &L) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
   static KernelSetup setup;
-  const int smem_max = 4 * G * 8 * 32 * W * VPT;         // the widest row of this variant
   int per_sm = 0;
-  auto *kern = rmsnorm_backward_kernel<T, TW, W, VPT>;
-  cudaError_t e = kernel_setup(setup, reinterpret_cast<const void *>(kern), NW * 32, smem_max,
+  auto *kern = rmsnorm_backward_kernel<T, TW, W, VPT, D>;
+  cudaError_t e = kernel_setup(setup, reinterpret_cast<const void *>(kern), NW * 32, 220 * 1024,
                                &per_sm);
   if (e != cudaSuccess) return e;
+  const int smem =
+      static_cast<int>((D * (dsum ? 3 : 2) * sizeof(T) + sizeof(float)) * G * cols);
+  // CTAs that an SM holds: by shared memory, and by 512 threads of 128 registers
+  int64_t fit = (228 * 1024) / (smem + 1024 + 512), most = NW <= 16 ? 512 / (NW * 32) : 1;
+  if (fit > most) fit = most;
+  if (fit < 1) fit = 1;
   const int64_t steps = (rows + G - 1) / G;
-  int64_t grid = static_cast<int64_t>(L.num_sms) * per_sm;
+  int64_t grid = static_cast<int64_t>(L.num_sms) * fit;
   if (grid > kNormParts) grid = kNormParts;
   if (grid > steps) grid = steps;
-  e = launch_dependent(kern, grid, NW * 32, static_cast<int>(4 * G * cols), 1, L,
-                       static_cast<const T *>(dy), ld_dy, static_cast<const T *>(s), ld_s,
-                       static_cast<const TW *>(weight), rstd, static_cast<const T *>(dsum),
-                       ld_dsum, rows, static_cast<int>(cols), static_cast<T *>(dx), part);
+  e = launch_dependent(kern, grid, NW * 32, smem, 1, L, static_cast<const T *>(dy), ld_dy,
+                       static_cast<const T *>(s), ld_s, static_cast<const TW *>(weight), rstd,
+                       static_cast<const T *>(dsum), ld_dsum, rows, static_cast<int>(cols),
+                       static_cast<T *>(dx), part);
   if (e != cudaSuccess) return e;
-  return launch_dependent(dweight_kernel, cols / 32, 256, 0, 1, L,
+  return launch_dependent(dweight_kernel, cols / 32, 1024, 0, 1, L,
                           static_cast<const float *>(part), static_cast<int>(grid),
                           static_cast<int>(cols), dweight);
 }
@@ -359,11 +566,17 @@ cudaError_t launch_bwd(const void *dy, int64_t ld_dy, const void *s, int64_t ld_
                        int64_t rows, int64_t cols, void *dx, float *dweight, float *part,
                        const Launch &L) {
   const int64_t n8 = cols / 8;
-  auto go = [&](auto w, auto v) {
-    return launch_bwd_t<T, TW, decltype(w)::value, decltype(v)::value>(
-        dy, ld_dy, s, ld_s, weight, rstd, dsum, ld_dsum, rows, cols, dx, dweight, part, L);
-  };
   using std::integral_constant;
+  auto go = [&](auto w, auto v) {
+    constexpr int W = decltype(w)::value, VPT = decltype(v)::value, G = W < 4 ? 4 / W : 1;
+    const int d = ring_depth((dsum ? 3 : 2) * G * cols * static_cast<int64_t>(sizeof(T)),
+                             G * cols * 4);
+    auto run = [&](auto depth) {
+      return launch_bwd_t<T, TW, W, VPT, decltype(depth)::value>(
+          dy, ld_dy, s, ld_s, weight, rstd, dsum, ld_dsum, rows, cols, dx, dweight, part, L);
+    };
+    return d == 3 ? run(integral_constant<int, 3>{}) : run(integral_constant<int, 0>{});
+  };
   if (n8 <= 64) return go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
   if (n8 <= 128) return go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
   if (n8 <= 256) return go(integral_constant<int, 4>{}, integral_constant<int, 2>{});

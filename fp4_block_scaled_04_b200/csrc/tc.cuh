@@ -14,10 +14,6 @@ namespace fp4q {
 
 constexpr long long kWaitCycles = 2000000000LL;  // ~1 s at the B200's clock
 
-__device__ __forceinline__ uint32_t smem_u32(const void *p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
 // Shared-memory matrix descriptor, K-major with 128-byte swizzle: rows of
 // 128 bytes, 8-row groups 1024 bytes apart (SBO), LBO 1 (unused for this
 // layout), descriptor version 1, layout type 2.
