@@ -153,18 +153,18 @@ __device__ __forceinline__ float row_sum(float v, float *slot, int warp) {
 // time, and walks the groups of rows blockIdx.x, + gridDim.x, ...  A thread keeps
 // up to VPT vectors of 8 values in registers: vector lane + 32 (warp in row) +
 // 32 W j, so a warp's loads are contiguous and the 4 lanes of a 32-value block are
-// neighbours.  DEPTH > 0: a ring of DEPTH groups in shared memory keeps loads in
+// neighbours.  RING: `depth` (2 or 3) groups in shared memory keep loads in
 // flight through the reduction and the stores (8192 x 4096 BF16 with a residual:
 // 39 us, 5.99 TB/s; 53 without it).  Rows too wide for it are loaded directly
-// (DEPTH 0).
-template <typename T, typename TW, int W, int VPT, int DEPTH, bool FULL>
+// instead.
+template <typename T, typename TW, int W, int VPT, bool RING, bool FULL>
 __global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
 rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int64_t ld_res,
                const TW *__restrict__ weight, float eps, int mode, uint8_t *__restrict__ q,
                uint8_t *__restrict__ sf, int scale_layout, float *__restrict__ rstd_out,
-               T *sum_out, T *__restrict__ y_out) {
+               T *sum_out, T *__restrict__ y_out, int depth) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
-  extern __shared__ __align__(16) uint8_t ring[];        // [DEPTH][x, residual][G] rows
+  extern __shared__ __align__(16) uint8_t ring[];        // [depth][x, residual][G] rows
   __shared__ __align__(16) float slot[2][NW];
   begin_dependent();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
@@ -204,9 +204,8 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
     cp_async_commit();
   };
   int64_t row = static_cast<int64_t>(blockIdx.x) * G + grp;
-  if constexpr (DEPTH > 0)
-#pragma unroll
-    for (int d = 0; d < DEPTH - 1; ++d) fetch(d, row + d * step);
+  if constexpr (RING)
+    for (int d = 0; d < depth - 1; ++d) fetch(d, row + d * step);
   Raw8<TW> wv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -221,9 +220,10 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
     const bool live = row < rows;
     const int64_t e0 = row * cols;
     uint8_t *const sf_at = sf + sf_row(row);
-    if constexpr (DEPTH > 0) {
-      fetch(stage == 0 ? DEPTH - 1 : stage - 1, row + (DEPTH - 1) * step);
-      cp_async_wait<DEPTH - 1>();
+    if constexpr (RING) {
+      fetch(stage == 0 ? depth - 1 : stage - 1, row + (depth - 1) * step);
+      if (depth == 3) cp_async_wait<2>();
+      else cp_async_wait<1>();
     }
     Raw8<T> s[VPT];
     float2 ss = both(0.0f);
@@ -232,7 +232,7 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
       const int v8 = lane + 32 * (wr + W * j);
       if (live && mine(v8)) {
         Raw8<T> rr;
-        if constexpr (DEPTH > 0) {
+        if constexpr (RING) {
           s[j] = ring_get<T>(ring + place(stage, 0), v8, n8);
           if (res) rr = ring_get<T>(ring + place(stage, 1), v8, n8);
         } else {
@@ -296,15 +296,19 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
       for (int64_t c = c0 + wr * 32 + lane; c < scols; c += W * 32)
         sf_at[sf_col(static_cast<int>(c))] = 0;
     }
-    if (++stage == DEPTH) stage = 0;
+    if (++stage == depth) stage = 0;
   }
   cp_async_wait<0>();
 }
 
-// The depth of the ring: 3 groups of rows of `bytes` each, where they fit next to
-// `fixed` bytes, else none.
+// The depth of a ring of groups of `bytes` each next to `fixed` bytes: 3 or 2
+// where two CTAs then fit an SM, else 3 or 2 for one (rows of 20 KB: 2 deep and two
+// CTAs beat 3 deep and one), else none.
 inline int ring_depth(int64_t bytes, int64_t fixed) {
-  return 3 * bytes + fixed <= 220 * 1024 ? 3 : 0;
+  for (const int64_t room : {112 * 1024, 220 * 1024})
+    for (int d = 3; d >= 2; --d)
+      if (d * bytes + fixed <= room) return d;
+  return 0;
 }
 
 template <typename T, typename TW>
@@ -313,19 +317,21 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
                        uint8_t *sf, int layout, float *rstd, void *sum, void *y,
                        const Launch &L) {
   const int64_t n8 = cols / 8, srows = scale_rows(rows, layout);
-  auto run = [&](auto w, auto v, auto d, auto full) {
-    constexpr int W = decltype(w)::value, VPT = decltype(v)::value, D = decltype(d)::value;
+  auto run = [&](auto w, auto v, auto ring, auto full) {
+    constexpr int W = decltype(w)::value, VPT = decltype(v)::value;
+    constexpr bool kRing = decltype(ring)::value;
     constexpr int NW = W < 4 ? 4 : W, G = NW / W;
-    auto *kern = rmsnorm_kernel<T, TW, W, VPT, D, decltype(full)::value>;
-    const int smem = static_cast<int>(D * (res ? 2 : 1) * G * cols * sizeof(T));
+    auto *kern = rmsnorm_kernel<T, TW, W, VPT, kRing, decltype(full)::value>;
+    const int64_t group = (res ? 2 : 1) * G * cols * static_cast<int64_t>(sizeof(T));
+    const int depth = kRing ? ring_depth(group, 0) : 0;
+    const int smem = static_cast<int>(depth * group);
     static KernelSetup setup;
     int per_sm = 0;
     cudaError_t e = kernel_setup(setup, reinterpret_cast<const void *>(kern), NW * 32,
-                                 D ? 220 * 1024 : 0, &per_sm);
+                                 kRing ? 220 * 1024 : 0, &per_sm);
     if (e != cudaSuccess) return e;
-    const int64_t steps = (srows + G - 1) / G;
-    int64_t grid = steps;                                // without a ring a row's CTA ends
-    if (D > 0) {
+    int64_t grid = (srows + G - 1) / G;                  // without a ring a row's CTA ends
+    if (kRing) {
       int64_t fit = (228 * 1024) / (smem + 1024 + 512);
       const int64_t threads = NW <= 16 ? 512 / (NW * 32) : 1;   // of 128 registers
       if (fit > threads) fit = threads;
@@ -334,35 +340,40 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
     return launch_dependent(kern, grid, NW * 32, smem, 1, L, static_cast<const T *>(x), rows,
                             static_cast<int>(cols), ld, static_cast<const T *>(res), ld_res,
                             static_cast<const TW *>(weight), eps, mode, q, sf, layout, rstd,
-                            static_cast<T *>(sum), static_cast<T *>(y));
+                            static_cast<T *>(sum), static_cast<T *>(y), depth);
   };
   using std::false_type;
   using std::integral_constant;
-  auto go = [&](auto w) {
-    constexpr int W = decltype(w)::value, G = W < 4 ? 4 / W : 1;
-    constexpr integral_constant<int, 4> vpt{};
-    if (ring_depth((res ? 2 : 1) * G * cols * static_cast<int64_t>(sizeof(T)), 0) == 0)
-      return run(w, vpt, integral_constant<int, 0>{}, false_type{});
-    if (cols == 256 * W * 4) return run(w, vpt, integral_constant<int, 3>{}, std::true_type{});
-    return run(w, vpt, integral_constant<int, 3>{}, false_type{});
-  };
-  // Few rows: each on as many warps as it has vectors, no ring.  Many: the fewest
-  // warps that hold a row in four vectors a thread, which spread the work that
-  // each row costs once over the most values (8192 x 4096 BF16: 39.4 us on four
-  // warps, 41.7 on eight, 55 on two).
+  using std::true_type;
+  constexpr integral_constant<int, 1> one{};
+  constexpr integral_constant<int, 3> three{};
+  constexpr integral_constant<int, 4> four{};
+  constexpr integral_constant<int, 5> five{};
+  // Few rows: each on as many warps as it has vectors, no ring.
   if (rows <= L.num_sms && n8 <= 1024) {
-    constexpr integral_constant<int, 1> one{};
-    constexpr integral_constant<int, 0> none{};
-    if (n8 <= 32) return run(integral_constant<int, 1>{}, one, none, false_type{});
-    if (n8 <= 128) return run(integral_constant<int, 4>{}, one, none, false_type{});
-    if (n8 <= 512) return run(integral_constant<int, 16>{}, one, none, false_type{});
-    return run(integral_constant<int, 32>{}, one, none, false_type{});
+    if (n8 <= 32) return run(one, one, false_type{}, false_type{});
+    if (n8 <= 128) return run(four, one, false_type{}, false_type{});
+    if (n8 <= 512) return run(integral_constant<int, 16>{}, one, false_type{}, false_type{});
+    return run(integral_constant<int, 32>{}, one, false_type{}, false_type{});
   }
-  if (n8 <= 128) return go(integral_constant<int, 1>{});
-  if (n8 <= 256) return go(integral_constant<int, 2>{});
-  if (n8 <= 512) return go(integral_constant<int, 4>{});
-  if (n8 <= 1024) return go(integral_constant<int, 8>{});
-  if (n8 <= 2048) return go(integral_constant<int, 16>{});
+  // Many: three to five vectors a thread, which spread the work that each row costs
+  // once over the most values (8192 x 4096 BF16: 39.4 us on four warps, 41.7 on
+  // eight, 55 on two).
+  auto go = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    if (n8 <= 32 * W * 3) return run(w, three, true_type{}, false_type{});
+    if (n8 == 32 * W * 4) return run(w, four, true_type{}, true_type{});
+    if (n8 == 32 * W * 5) return run(w, five, true_type{}, true_type{});
+    if (n8 < 32 * W * 4) return run(w, four, true_type{}, false_type{});
+    return run(w, five, true_type{}, false_type{});
+  };
+  if (n8 <= 160) return go(one);
+  if (n8 <= 320) return go(integral_constant<int, 2>{});
+  if (n8 <= 640) return go(four);
+  if (n8 <= 1280) return go(integral_constant<int, 8>{});
+  if (ring_depth((res ? 2 : 1) * cols * static_cast<int64_t>(sizeof(T)), 0) == 0)
+    return run(integral_constant<int, 32>{}, four, false_type{}, false_type{});
+  if (n8 <= 2560) return go(integral_constant<int, 16>{});
   return go(integral_constant<int, 32>{});
 }
 
@@ -372,20 +383,20 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
 // dweight_kernel.  Rows come through the ring where it fits (8192 x 4096 BF16 with
 // dsum: 45.5 us with dweight_kernel, 5.9 TB/s; 49-60 in direct forms, which
 // alternate between loading and computing).
-template <typename T, typename TW, int W, int VPT, int DEPTH>
+template <typename T, typename TW, int W, int VPT, bool RING>
 __global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
 rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s, int64_t ld_s,
                         const TW *__restrict__ weight, const float *__restrict__ rstd,
                         const T *dsum, int64_t ld_dsum, int64_t rows, int cols, T *dx,
-                        float *__restrict__ part) {
+                        float *__restrict__ part, int depth) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
-  extern __shared__ __align__(16) uint8_t ring[];        // [DEPTH][dy, s, dsum][G] rows, [G] dw
+  extern __shared__ __align__(16) uint8_t ring[];        // [depth][dy, s, dsum][G] rows, [G] dw
   __shared__ __align__(16) float slot[2][NW];
   begin_dependent();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
   const int n8 = cols / 8;
   const int row_bytes = cols * static_cast<int>(sizeof(T)), tensors = dsum ? 3 : 2;
-  float *dw = reinterpret_cast<float *>(ring + static_cast<size_t>(DEPTH) * tensors * G * row_bytes);
+  float *dw = reinterpret_cast<float *>(ring + static_cast<size_t>(RING ? depth : 0) * tensors * G * row_bytes);
   // this row's part, in two planes of float4 as the ring's
   uint8_t *mine = reinterpret_cast<uint8_t *>(dw + grp * cols);
 #pragma unroll
@@ -414,9 +425,8 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s, int
     cp_async_commit();
   };
   int64_t row = static_cast<int64_t>(blockIdx.x) * G + grp;
-  if constexpr (DEPTH > 0)
-#pragma unroll
-    for (int d = 0; d < DEPTH - 1; ++d) fetch(d, row + d * step);
+  if constexpr (RING)
+    for (int d = 0; d < depth - 1; ++d) fetch(d, row + d * step);
   Raw8<TW> wv[VPT];
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -430,16 +440,17 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s, int
        row0 += step, row += step, turn ^= 1) {
     const bool live = row < rows;
     const float r = live ? rstd[row] : 0.0f;
-    if constexpr (DEPTH > 0) {
-      fetch(stage == 0 ? DEPTH - 1 : stage - 1, row + (DEPTH - 1) * step);
-      cp_async_wait<DEPTH - 1>();
+    if constexpr (RING) {
+      fetch(stage == 0 ? depth - 1 : stage - 1, row + (depth - 1) * step);
+      if (depth == 3) cp_async_wait<2>();
+      else cp_async_wait<1>();
     }
     Raw8<T> gv[VPT], sv[VPT], dv[VPT];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v8 = lane + 32 * (wr + W * j);
       if (live && v8 < n8) {
-        if constexpr (DEPTH > 0) {
+        if constexpr (RING) {
           gv[j] = ring_get<T>(ring + place(stage, 0), v8, n8);
           sv[j] = ring_get<T>(ring + place(stage, 1), v8, n8);
           if (dsum) dv[j] = ring_get<T>(ring + place(stage, 2), v8, n8);
@@ -495,7 +506,7 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s, int
         out.store(dx + row * cols + 8 * v8);
       }
     }
-    if (++stage == DEPTH) stage = 0;
+    if (++stage == depth) stage = 0;
   }
   cp_async_wait<0>();
   __syncthreads();
@@ -528,7 +539,7 @@ dweight_kernel(const float *part, int parts, int cols, float *dweight) {
   }
 }
 
-template <typename T, typename TW, int W, int VPT, int D>
+template <typename T, typename TW, int W, int VPT, bool RING>
 cudaError_t launch_bwd_t(const void *dy, int64_t ld_dy, const void *s, int64_t ld_s,
                          const void *weight, const float *rstd, const void *dsum,
                          int64_t ld_dsum, int64_t rows, int64_t cols, void *dx, float *dweight,
@@ -536,12 +547,14 @@ cudaError_t launch_bwd_t(const void *dy, int64_t ld_dy, const void *s, int64_t l
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
   static KernelSetup setup;
   int per_sm = 0;
-  auto *kern = rmsnorm_backward_kernel<T, TW, W, VPT, D>;
+  auto *kern = rmsnorm_backward_kernel<T, TW, W, VPT, RING>;
   cudaError_t e = kernel_setup(setup, reinterpret_cast<const void *>(kern), NW * 32, 220 * 1024,
                                &per_sm);
   if (e != cudaSuccess) return e;
-  const int smem =
-      static_cast<int>((D * (dsum ? 3 : 2) * sizeof(T) + sizeof(float)) * G * cols);
+  const int64_t group = (dsum ? 3 : 2) * G * cols * static_cast<int64_t>(sizeof(T));
+  const int64_t parts = G * cols * static_cast<int64_t>(sizeof(float));
+  const int depth = RING ? ring_depth(group, parts) : 0;
+  const int smem = static_cast<int>(depth * group + parts);
   // CTAs that an SM holds: by shared memory, and by 512 threads of 128 registers
   int64_t fit = (228 * 1024) / (smem + 1024 + 512), most = NW <= 16 ? 512 / (NW * 32) : 1;
   if (fit > most) fit = most;
@@ -553,7 +566,7 @@ cudaError_t launch_bwd_t(const void *dy, int64_t ld_dy, const void *s, int64_t l
   e = launch_dependent(kern, grid, NW * 32, smem, 1, L, static_cast<const T *>(dy), ld_dy,
                        static_cast<const T *>(s), ld_s, static_cast<const TW *>(weight), rstd,
                        static_cast<const T *>(dsum), ld_dsum, rows, static_cast<int>(cols),
-                       static_cast<T *>(dx), part);
+                       static_cast<T *>(dx), part, depth);
   if (e != cudaSuccess) return e;
   return launch_dependent(dweight_kernel, cols / 32, 1024, 0, 1, L,
                           static_cast<const float *>(part), static_cast<int>(grid),
@@ -567,23 +580,28 @@ cudaError_t launch_bwd(const void *dy, int64_t ld_dy, const void *s, int64_t ld_
                        const Launch &L) {
   const int64_t n8 = cols / 8;
   using std::integral_constant;
-  auto go = [&](auto w, auto v) {
-    constexpr int W = decltype(w)::value, VPT = decltype(v)::value, G = W < 4 ? 4 / W : 1;
-    const int d = ring_depth((dsum ? 3 : 2) * G * cols * static_cast<int64_t>(sizeof(T)),
-                             G * cols * 4);
-    auto run = [&](auto depth) {
-      return launch_bwd_t<T, TW, W, VPT, decltype(depth)::value>(
-          dy, ld_dy, s, ld_s, weight, rstd, dsum, ld_dsum, rows, cols, dx, dweight, part, L);
-    };
-    return d == 3 ? run(integral_constant<int, 3>{}) : run(integral_constant<int, 0>{});
+  auto run = [&](auto w, auto v, auto ring) {
+    return launch_bwd_t<T, TW, decltype(w)::value, decltype(v)::value, decltype(ring)::value>(
+        dy, ld_dy, s, ld_s, weight, rstd, dsum, ld_dsum, rows, cols, dx, dweight, part, L);
   };
-  if (n8 <= 64) return go(integral_constant<int, 1>{}, integral_constant<int, 2>{});
-  if (n8 <= 128) return go(integral_constant<int, 2>{}, integral_constant<int, 2>{});
-  if (n8 <= 256) return go(integral_constant<int, 4>{}, integral_constant<int, 2>{});
-  if (n8 <= 512) return go(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  if (n8 <= 1024) return go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  if (n8 <= 2048) return go(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  return go(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  constexpr integral_constant<int, 2> two{};
+  constexpr integral_constant<int, 3> three{};
+  auto go = [&](auto w) {
+    constexpr int W = decltype(w)::value;
+    if (n8 <= 32 * W * 2) return run(w, two, std::true_type{});
+    return run(w, three, std::true_type{});
+  };
+  if (n8 <= 96) return go(integral_constant<int, 1>{});
+  if (n8 <= 192) return go(two);
+  if (n8 <= 384) return go(integral_constant<int, 4>{});
+  if (n8 <= 768) return go(integral_constant<int, 8>{});
+  const int64_t row = cols * static_cast<int64_t>(sizeof(T));
+  if (ring_depth((dsum ? 3 : 2) * row, cols * 4) == 0) {
+    if (n8 <= 2048) return run(integral_constant<int, 32>{}, two, std::false_type{});
+    return run(integral_constant<int, 32>{}, integral_constant<int, 4>{}, std::false_type{});
+  }
+  if (n8 <= 1536) return go(integral_constant<int, 16>{});
+  return go(integral_constant<int, 32>{});
 }
 
 }  // namespace
