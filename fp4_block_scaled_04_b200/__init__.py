@@ -298,24 +298,23 @@ def fp4q_quantize_mxfp6(x: torch.Tensor, fp6_format: int = FP6_E2M3, e8m0_mode: 
     return out
 
 
-def fp4q_quantize_mxfp8(x: torch.Tensor, e8m0_mode: int = E8M0_CEIL,
-                        scale_layout: int = SCALE_LINEAR, out: dict | None = None) -> dict:
-    """MXFP8 1x32 row-wise; returns {'q': [rows, cols] E4M3 codes, 'sf'}.  Any
-    shape with cols % 32 == 0 may be swizzled (the padding is written as 0)."""
-    rows, cols, ld = _matrix(x)
-    dev = x.device
-    if out is None:
-        out = {"q": _u8((rows, cols), dev),
-               "sf": _u8(fp4q_scale_bytes(rows, cols, 32, scale_layout), dev)}
-    else:
-        _check_mxfp8_out(out, rows, cols, scale_layout, dev)
-    _check("fp4q_quantize_mxfp8", lib().fp4q_quantize_mxfp8(
-        _ptr(x), _dtype(x), rows, cols, ld, e8m0_mode, _ptr(out["q"]), _ptr(out["sf"]),
-        scale_layout, _stream(dev)))
-    return out
+def _addr(t: torch.Tensor | None):
+    """A device address as ctypes takes it for a pointer argument."""
+    return None if t is None else t.data_ptr()
 
 
-def _expect(t: torch.Tensor | None, name: str, shape: tuple, dtypes, device) -> None:
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _mx_scale_bytes(rows: int, cols: int, scale_layout: int) -> int:
+    """fp4q_scale_bytes(rows, cols, 32, scale_layout) without the call."""
+    if scale_layout == SCALE_LINEAR:
+        return rows * (cols // 32)
+    return (rows + 127) // 128 * 128 * ((cols // 32 + 3) // 4 * 4)
+
+
+def _expect(t: torch.Tensor | None, name: str, shape: tuple, dtypes: tuple, device) -> None:
     """A dense tensor of this shape, one of these dtypes, on this device (None passes)."""
     if t is None:
         return
@@ -323,7 +322,7 @@ def _expect(t: torch.Tensor | None, name: str, shape: tuple, dtypes, device) -> 
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got "
                          f"shape {tuple(t.shape)}, strides {t.stride()}")
 
@@ -336,9 +335,9 @@ def _expect_bytes(t: torch.Tensor, name: str, n: int, device) -> None:
         raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {n} bytes")
 
 
-def _check_mxfp8_out(out: dict, rows: int, cols: int, scale_layout: int, device) -> None:
-    _expect(out["q"], "out['q']", (rows, cols), (torch.uint8,), device)
-    _expect_bytes(out["sf"], "out['sf']", fp4q_scale_bytes(rows, cols, 32, scale_layout), device)
+_U8 = (torch.uint8,)
+_F32 = (torch.float32,)
+_FLOATS = (torch.bfloat16, torch.float32)
 
 
 def _like(t: torch.Tensor | None, x: torch.Tensor, name: str) -> int:
@@ -351,34 +350,54 @@ def _like(t: torch.Tensor | None, x: torch.Tensor, name: str) -> int:
     return _matrix(t, name)[2]
 
 
+def fp4q_quantize_mxfp8(x: torch.Tensor, e8m0_mode: int = E8M0_CEIL,
+                        scale_layout: int = SCALE_LINEAR, out: dict | None = None) -> dict:
+    """MXFP8 1x32 row-wise; returns {'q': [rows, cols] E4M3 codes, 'sf'}.  Any
+    shape with cols % 32 == 0 may be swizzled (the padding is written as 0)."""
+    rows, cols, ld = _matrix(x)
+    dev = x.device
+    n = _mx_scale_bytes(rows, cols, scale_layout)
+    if out is None:
+        out = {"q": _u8((rows, cols), dev), "sf": _u8(n, dev)}
+    else:
+        _expect(out["q"], "out['q']", (rows, cols), _U8, dev)
+        _expect_bytes(out["sf"], "out['sf']", n, dev)
+    _check("fp4q_quantize_mxfp8", lib().fp4q_quantize_mxfp8(
+        x.data_ptr(), _dtype(x), rows, cols, ld, e8m0_mode, out["q"].data_ptr(),
+        out["sf"].data_ptr(), scale_layout, _raw_stream(dev)))
+    return out
+
+
 def fp4q_rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
                        residual: torch.Tensor | None = None, e8m0_mode: int = E8M0_CEIL,
                        scale_layout: int = SCALE_LINEAR, want_y: bool = False,
                        out: dict | None = None) -> dict:
     """RMS norm of s = x + residual (or x) in MXFP8; returns {'q', 'sf', 'rstd'
     [rows] FP32, 'sum' (with a residual: s in x's dtype), 'y' (with want_y: the
-    normed values in x's dtype)}.  out['sum'] may be x or residual itself."""
+    normed values in x's dtype)}.  out['sum'] may be x or residual itself.  With
+    ``out``, what it holds is written (want_y is not looked at)."""
     rows, cols, ld = _matrix(x)
     ld_res = _like(residual, x, "residual")
     dev = x.device
-    _expect(weight, "weight", (cols,), (torch.bfloat16, torch.float32), dev)
+    _expect(weight, "weight", (cols,), _FLOATS, dev)
+    n = _mx_scale_bytes(rows, cols, scale_layout)
     if out is None:
-        out = {"q": _u8((rows, cols), dev),
-               "sf": _u8(fp4q_scale_bytes(rows, cols, 32, scale_layout), dev),
+        out = {"q": _u8((rows, cols), dev), "sf": _u8(n, dev),
                "rstd": torch.empty(rows, dtype=torch.float32, device=dev)}
         if residual is not None:
             out["sum"] = torch.empty((rows, cols), dtype=x.dtype, device=dev)
         if want_y:
             out["y"] = torch.empty((rows, cols), dtype=x.dtype, device=dev)
     else:
-        _check_mxfp8_out(out, rows, cols, scale_layout, dev)
-        _expect(out.get("rstd"), "out['rstd']", (rows,), (torch.float32,), dev)
+        _expect(out["q"], "out['q']", (rows, cols), _U8, dev)
+        _expect_bytes(out["sf"], "out['sf']", n, dev)
+        _expect(out.get("rstd"), "out['rstd']", (rows,), _F32, dev)
         _expect(out.get("sum"), "out['sum']", (rows, cols), (x.dtype,), dev)
         _expect(out.get("y"), "out['y']", (rows, cols), (x.dtype,), dev)
     _check("fp4q_rmsnorm_mxfp8", lib().fp4q_rmsnorm_mxfp8(
-        _ptr(x), _dtype(x), rows, cols, ld, _ptr(residual), ld_res, _ptr(weight), _dtype(weight),
-        eps, e8m0_mode, _ptr(out["q"]), _ptr(out["sf"]), scale_layout, _ptr(out.get("rstd")),
-        _ptr(out.get("sum")), _ptr(out.get("y")), _stream(dev)))
+        x.data_ptr(), _dtype(x), rows, cols, ld, _addr(residual), ld_res, weight.data_ptr(),
+        _dtype(weight), eps, e8m0_mode, out["q"].data_ptr(), out["sf"].data_ptr(), scale_layout,
+        _addr(out.get("rstd")), _addr(out.get("sum")), _addr(out.get("y")), _raw_stream(dev)))
     return out
 
 
@@ -392,23 +411,23 @@ def fp4q_rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     rows, cols, ld = _matrix(x)
     ld_dy, ld_dsum = _like(dy, x, "dy"), _like(dsum, x, "dsum")
     dev = x.device
-    _expect(weight, "weight", (cols,), (torch.bfloat16, torch.float32), dev)
-    _expect(rstd, "rstd", (rows,), (torch.float32,), dev)
+    _expect(weight, "weight", (cols,), _FLOATS, dev)
+    _expect(rstd, "rstd", (rows,), _F32, dev)
     if out is None:
         out = {"dx": torch.empty((rows, cols), dtype=x.dtype, device=dev),
                "dweight": torch.empty(cols, dtype=torch.float32, device=dev)}
     else:
         _expect(out["dx"], "out['dx']", (rows, cols), (x.dtype,), dev)
-        _expect(out["dweight"], "out['dweight']", (cols,), (torch.float32,), dev)
-    need = int(lib().fp4q_rmsnorm_backward_workspace_bytes(rows, cols))
+        _expect(out["dweight"], "out['dweight']", (cols,), _F32, dev)
+    need = lib().fp4q_rmsnorm_backward_workspace_bytes(rows, cols)
     if workspace is None:
         workspace = _u8(need, dev)
     else:
         _expect_bytes(workspace, "workspace", need, dev)
     _check("fp4q_rmsnorm_backward", lib().fp4q_rmsnorm_backward(
-        _ptr(dy), ld_dy, _ptr(x), ld, _dtype(x), _ptr(weight), _dtype(weight), _ptr(rstd),
-        _ptr(dsum), ld_dsum, rows, cols, _ptr(out["dx"]), _ptr(out["dweight"]), _ptr(workspace),
-        workspace.numel(), _stream(dev)))
+        dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype(x), weight.data_ptr(), _dtype(weight),
+        rstd.data_ptr(), _addr(dsum), ld_dsum, rows, cols, out["dx"].data_ptr(),
+        out["dweight"].data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
     return out
 
 
@@ -490,10 +509,10 @@ def _matrix_out(out: torch.Tensor | None, rows: int, cols: int, dtype: torch.dty
     return out, _dtype(out), _matrix(out, "out")[2]
 
 
-def _status_ptr(status: torch.Tensor | None, device):
+def _status_addr(status: torch.Tensor | None, device):
     if status is not None and (status.dtype != torch.int32 or status.device != device):
         raise ValueError(f"status must be an int32 tensor on {device}")
-    return _ptr(status)
+    return _addr(status)
 
 
 def fp4q_gemm_mxfp8_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor,
@@ -505,19 +524,18 @@ def fp4q_gemm_mxfp8_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor,
     fp4q_quantize_mxfp8 / fp4q_rmsnorm_mxfp8 and fp4q_quantize_mxfp4 write them)."""
     if not qa.is_cuda:
         raise ValueError("qa must be a CUDA tensor")
-    if qa.dim() != 2 or qb.dim() != 2 or qa.shape[1] != 2 * qb.shape[1]:
-        raise ValueError("qa must be [M, K] and qb [N, K/2], got "
-                         f"{tuple(qa.shape)} and {tuple(qb.shape)}")
+    if qa.dim() != 2 or qb.dim() != 2:
+        raise ValueError("qa must be [M, K] and qb [N, K/2]")
     (M, K), N, dev = qa.shape, qb.shape[0], qa.device
-    _expect(qa, "qa", (M, K), (torch.uint8,), dev)
-    _expect(qb, "qb", (N, K // 2), (torch.uint8,), dev)
-    if K % 32 == 0:
-        _expect_bytes(sfa, "sfa", fp4q_scale_bytes(M, K, 32, SCALE_SWIZZLED), dev)
-        _expect_bytes(sfb, "sfb", fp4q_scale_bytes(N, K, 32, SCALE_SWIZZLED), dev)
+    _expect(qa, "qa", (M, K), _U8, dev)
+    _expect(qb, "qb", (N, K // 2), _U8, dev)
+    if K % 128 == 0:
+        _expect_bytes(sfa, "sfa", _mx_scale_bytes(M, K, SCALE_SWIZZLED), dev)
+        _expect_bytes(sfb, "sfb", _mx_scale_bytes(N, K, SCALE_SWIZZLED), dev)
     c, cdt, ldc = _matrix_out(out, M, N, out_dtype, dev)
     _check("fp4q_gemm_mxfp8_mxfp4", lib().fp4q_gemm_mxfp8_mxfp4(
-        _ptr(qa), _ptr(sfa), _ptr(qb), _ptr(sfb), M, N, K, _ptr(c), cdt, ldc,
-        _status_ptr(status, dev), _stream(dev)))
+        qa.data_ptr(), sfa.data_ptr(), qb.data_ptr(), sfb.data_ptr(), M, N, K, c.data_ptr(), cdt,
+        ldc, _status_addr(status, dev), _raw_stream(dev)))
     return c
 
 
@@ -534,24 +552,25 @@ def fp4q_moe_mxfp4(xq: torch.Tensor, xsf: torch.Tensor, logits: torch.Tensor,
     if xq.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
         raise ValueError("xq must be [T, H], w13 [E, 2I, H/2] and w2 [E, H, I/2]")
     (T, H), (E, I), dev = xq.shape, (w13.shape[0], w13.shape[1] // 2), xq.device
-    _expect(xq, "xq", (T, H), (torch.uint8,), dev)
-    _expect(logits, "logits", (T, E), (torch.float32, torch.bfloat16), dev)
-    _expect(w13, "w13", (E, 2 * I, H // 2), (torch.uint8,), dev)
-    _expect(w2, "w2", (E, H, I // 2), (torch.uint8,), dev)
+    _expect(xq, "xq", (T, H), _U8, dev)
+    _expect(logits, "logits", (T, E), _FLOATS, dev)
+    _expect(w13, "w13", (E, 2 * I, H // 2), _U8, dev)
+    _expect(w2, "w2", (E, H, I // 2), _U8, dev)
     if H % 32 == 0 and I % 32 == 0:
-        _expect_bytes(xsf, "xsf", fp4q_scale_bytes(T, H, 32, SCALE_SWIZZLED), dev)
-        _expect_bytes(sf13, "sf13", fp4q_scale_bytes(E * 2 * I, H, 32, SCALE_SWIZZLED), dev)
-        _expect_bytes(sf2, "sf2", fp4q_scale_bytes(E * H, I, 32, SCALE_SWIZZLED), dev)
+        _expect_bytes(xsf, "xsf", _mx_scale_bytes(T, H, SCALE_SWIZZLED), dev)
+        _expect_bytes(sf13, "sf13", _mx_scale_bytes(E * 2 * I, H, SCALE_SWIZZLED), dev)
+        _expect_bytes(sf2, "sf2", _mx_scale_bytes(E * H, I, SCALE_SWIZZLED), dev)
     c, cdt, ldo = _matrix_out(out, T, H, out_dtype, dev)
-    need = int(lib().fp4q_moe_mxfp4_workspace_bytes(T, E, top_k, H, I))
+    need = lib().fp4q_moe_mxfp4_workspace_bytes(T, E, top_k, H, I)
     if workspace is None:
         workspace = _u8(need, dev)
     else:
         _expect_bytes(workspace, "workspace", need, dev)
     _check("fp4q_moe_mxfp4", lib().fp4q_moe_mxfp4(
-        _ptr(xq), _ptr(xsf), _ptr(logits), _dtype(logits), _ptr(w13), _ptr(sf13), _ptr(w2),
-        _ptr(sf2), T, E, top_k, H, I, int(bool(renormalize)), _ptr(c), cdt, ldo, _ptr(workspace),
-        workspace.numel(), _status_ptr(status, dev), _stream(dev)))
+        xq.data_ptr(), xsf.data_ptr(), logits.data_ptr(), _dtype(logits), w13.data_ptr(),
+        sf13.data_ptr(), w2.data_ptr(), sf2.data_ptr(), T, E, top_k, H, I,
+        int(bool(renormalize)), c.data_ptr(), cdt, ldo, workspace.data_ptr(), workspace.numel(),
+        _status_addr(status, dev), _raw_stream(dev)))
     return c
 
 
