@@ -803,6 +803,7 @@ fp4q_status fp4q_rmsnorm_mxfp8(const void *x, int dtype, int64_t rows, int64_t c
   // an in-place sum needs the same place for every element
   if (sum && ((sum == x && ld != cols) || (sum == residual && ld_residual != cols)))
     return FP4Q_ERR_INVALID_ARG;
+  if (y && (y == x || y == residual || y == sum)) return FP4Q_ERR_INVALID_ARG;
   Launch L;
   FP4Q_TRY(bind_device(x, stream, &L));
   FP4Q_TRY(check_dev(residual, true));

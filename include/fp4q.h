@@ -379,7 +379,8 @@ fp4q_status fp4q_quantize_mxfp8(const void *x, int dtype, int64_t rows, int64_t 
  *   rstd         [rows] floats, or NULL
  *   sum          [rows, cols] of dtype <- s, or NULL; it may be x or residual
  *                itself when that is dense (leading dimension cols)
- *   y            [rows, cols] of dtype <- RN_T(y), or NULL (for a router)
+ *   y            [rows, cols] of dtype <- RN_T(y), or NULL (for a router); not
+ *                x, residual or sum
  *   eps          >= 0
  * Shape: cols % 32 == 0, cols <= 32768.  All pointers 16-byte aligned. */
 fp4q_status fp4q_rmsnorm_mxfp8(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ld,

@@ -53,6 +53,8 @@ def test_norm(L):
         assert norm(L, **{k: ODD}) == ALIGN
     assert norm(L, s=A, ld=128) == ARG                 # in place, but not at the same places
     assert norm(L, s=A2, ld_res=128) == ARG
+    assert norm(L, y=A) == ARG and norm(L, y=A2) == ARG
+    assert norm(L, s=ctypes.c_void_p(0x7F2000000000), y=ctypes.c_void_p(0x7F2000000000)) == ARG
     assert norm(L, rows=0) == OK
 
 
