@@ -433,8 +433,8 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
           const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s;
           const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
           if (elect_one()) {
-            mma_ktile_mx4x8<1>(tmem + (2 * b + half) * BN, dw + at, dx + at, dsf + at,
-                               dsf + at + 32, sf, sf + 4, 0, idesc, kt != k0);
+            mma_ktile_mx4x8(tmem + (2 * b + half) * BN, dw + at, dx + at, dsf + at, dsf + at + 32,
+                            sf, sf + 4, idesc, kt != k0);
             tc_commit(bars.empty + 8 * ring.s);
             if (half == 1 && kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
           }
@@ -640,8 +640,8 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
         const uint32_t sf = tmem + C::SF_COL0 + C::SF_COLS * ring.s;
         const uint32_t at = ring.s * (C::STAGE_BYTES / 16);
         if (elect_one()) {
-          mma_ktile_mx4x8<1>(tmem + b * BN, dw + at, dx + at, dsf + at, dsf + at + 32, sf, sf + 4,
-                             0, idesc, kt != k0);
+          mma_ktile_mx4x8(tmem + b * BN, dw + at, dx + at, dsf + at, dsf + at + 32, sf, sf + 4,
+                          idesc, kt != k0);
           tc_commit(bars.empty + 8 * ring.s);
           if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
         }

@@ -176,22 +176,17 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   return true;
 }
 
-// The MMAs of one K-tile of 128 values: the scale tiles of A (128 rows) and B
-// (NSFB tiles of 128 columns; 0: B's are there already) into tensor memory at
-// sfa and sfb, four MMAs; B's first column has its scales `skip` columns of
-// tensor memory (32 tokens each) into its tiles.  Issued by one elected lane.
-template <int NSFB>
+// The MMAs of one K-tile of 128 values: the scale tiles of A and B (128 rows each)
+// into tensor memory at sfa and sfb, four MMAs.  Issued by one elected lane.
 __device__ __forceinline__ void mma_ktile_mx4x8(uint32_t d, uint64_t da, uint64_t db,
                                                 uint64_t dsfa, uint64_t dsfb, uint32_t sfa,
-                                                uint32_t sfb, uint32_t skip, uint32_t idesc,
-                                                bool accumulate) {
+                                                uint32_t sfb, uint32_t idesc, bool accumulate) {
   tc_copy_sf(sfa, dsfa);
-#pragma unroll
-  for (int h = 0; h < NSFB; ++h) tc_copy_sf(sfb + 4u * h, dsfb + 32u * h);   // 512 bytes on
+  tc_copy_sf(sfb, dsfb);
 #pragma unroll
   for (uint32_t k = 0; k < 4; ++k)                       // 32 values = 32 bytes = 2 units
     tc_mma_mx4x8(d, da + 2u * k, db + 2u * k, idesc | (k << 29) | (k << 4), sfa | (k << 30),
-                 (sfb + skip) | (k << 30), accumulate || k != 0);
+                 sfb | (k << 30), accumulate || k != 0);
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -254,16 +249,19 @@ __device__ __forceinline__ void put4(__nv_bfloat16 *p, float4 v) {
   *reinterpret_cast<uint2 *>(p) = w;
 }
 
-// The sum over a cluster of S <= 8 CTAs of their [tokens][128] FP32 parts at
-// shared-memory address `at`, in rank order, to dst[token * ld + row]: tokens in
-// turn over the ranks and the `warps` warps that call this (warp = 0, 1, ...),
-// four rows a lane.  All S loads of a token are in flight together.
+// The sum over S <= 8 CTAs of a cluster (ranks base, base + step, ...; this one is
+// number `rank` of them) of their [tokens][128] FP32 parts at shared-memory address
+// `at`, in that order, to dst[token * ld + row]: tokens in turn over the CTAs and
+// the `warps` warps that call this (warp = 0, 1, ...), four rows a lane.  All S
+// loads of a token are in flight together.
 template <typename OutT>
 __device__ __forceinline__ void cluster_sum(uint32_t at, int tokens, int S, int rank, int warp,
-                                            int warps, int lane, OutT *dst, int64_t ld) {
+                                            int warps, int lane, OutT *dst, int64_t ld,
+                                            int base = 0, int step = 1) {
   uint32_t peer[8];
 #pragma unroll
-  for (int p = 0; p < 8; ++p) peer[p] = peer_smem(at, p < S ? p : 0) + 16 * lane;
+  for (int p = 0; p < 8; ++p)
+    peer[p] = peer_smem(at, base + step * (p < S ? p : 0)) + 16 * lane;
 #pragma unroll 2
   for (int t = rank + S * warp; t < tokens; t += S * warps) {
     float4 v[8];
@@ -277,6 +275,86 @@ __device__ __forceinline__ void cluster_sum(uint32_t at, int tokens, int S, int 
                            __fadd_rn(v[0].z, v[p].z), __fadd_rn(v[0].w, v[p].w));
     put4(dst + t * ld + 4 * lane, v[0]);
   }
+}
+
+// ---------------------------------------------------------------------------
+// the pair form: two CTAs (cluster ranks 2i, the leader, and 2i + 1) share one
+// MMA of M = 256, each with its half of both operands and its 128 lanes of the
+// accumulator (cta_group::2).  No load uses cluster multicast.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// warp_wait on a barrier at which CTAs of the cluster arrive
+__device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity) {
+  if (__all_sync(0xFFFFFFFFu, mbar_test_cluster(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (!__all_sync(0xFFFFFFFFu, mbar_test_cluster(bar, parity)))
+    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitCycles)) return false;
+  return true;
+}
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t peer_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_bar)
+               : "memory");
+}
+// a load into this CTA's shared memory that completes on the leader's barrier
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x,
+                                                 int y, uint32_t leader_bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(leader_bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_copy_sf_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+__device__ __forceinline__ void tc_mma_mx4x8_pair(uint32_t d, uint64_t a, uint64_t b,
+                                                  uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                                  uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, %3, [%5], "
+      "[%6], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+      : "memory");
+}
+// arrives on the barrier at this offset in both CTAs of the pair (leader's rank
+// `leader` in the cluster) when the MMAs so far are complete
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint32_t leader) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3u << leader))
+      : "memory");
+}
+// mma_ktile_mx4x8 for the pair: idesc with M = 256; B's scales are two tiles, and
+// those of its first column lie `skip` columns (32 tokens each) into them
+__device__ __forceinline__ void mma_ktile_mx4x8_pair(uint32_t d, uint64_t da, uint64_t db,
+                                                     uint64_t dsf, uint32_t sf, uint32_t skip,
+                                                     uint32_t idesc, bool accumulate) {
+  tc_copy_sf_pair(sf, dsf);
+  tc_copy_sf_pair(sf + 4, dsf + 32);
+  tc_copy_sf_pair(sf + 8, dsf + 64);
+#pragma unroll
+  for (uint32_t k = 0; k < 4; ++k)
+    tc_mma_mx4x8_pair(d, da + 2u * k, db + 2u * k, idesc | (k << 29) | (k << 4), sf | (k << 30),
+                      (sf + 4 + skip) | (k << 30), accumulate || k != 0);
 }
 
 // cuTensorMapEncodeTiled, reached through the runtime (no link to the driver
@@ -323,6 +401,20 @@ inline bool make_map_mxfp8(CUtensorMap *map, const uint8_t *base, int64_t rows, 
   const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides,
              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// A matrix of 512-byte scale tiles read as boxes of one tile (two rows of 256
+// bytes); tiles past the end read as 0.
+inline bool make_map_scales(CUtensorMap *map, const uint8_t *base, int64_t tiles) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(2 * tiles)};
+  const cuuint64_t strides[1] = {256};
+  const cuuint32_t box[2] = {256, 2}, estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
