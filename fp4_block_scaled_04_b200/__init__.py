@@ -303,8 +303,7 @@ def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+_raw_stream = torch._C._cuda_getCurrentRawStream      # of a device index, as an integer
 
 
 def _mx_scale_bytes(rows: int, cols: int, scale_layout: int) -> int:
@@ -314,25 +313,29 @@ def _mx_scale_bytes(rows: int, cols: int, scale_layout: int) -> int:
     return (rows + 127) // 128 * 128 * ((cols // 32 + 3) // 4 * 4)
 
 
-def _expect(t: torch.Tensor | None, name: str, shape: tuple, dtypes: tuple, device) -> None:
-    """A dense tensor of this shape, one of these dtypes, on this device (None passes)."""
-    if t is None:
+def _expect(t: torch.Tensor | None, name: str, shape: tuple, dtypes: tuple, index: int) -> None:
+    """A dense tensor of this shape, one of these dtypes, on this CUDA device (None
+    passes).  One expression in the good case: a one-token call spends more time on
+    the host than on the GPU."""
+    if t is None or (t.get_device() == index and t.dtype in dtypes and t.shape == shape
+                     and t.is_contiguous()):
         return
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {list(dtypes)}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got "
-                         f"shape {tuple(t.shape)}, strides {t.stride()}")
+    raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)}, got "
+                     f"shape {tuple(t.shape)}, strides {t.stride()}")
 
 
-def _expect_bytes(t: torch.Tensor, name: str, n: int, device) -> None:
-    """A dense uint8 buffer of at least n bytes on this device."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {n} bytes")
+def _expect_bytes(t: torch.Tensor, name: str, n: int, index: int) -> None:
+    """A dense uint8 buffer of at least n bytes on this CUDA device."""
+    if (t.get_device() == index and t.dtype is torch.uint8 and t.numel() >= n
+            and t.is_contiguous()):
+        return
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {n} bytes")
 
 
 _U8 = (torch.uint8,)
@@ -344,7 +347,7 @@ def _like(t: torch.Tensor | None, x: torch.Tensor, name: str) -> int:
     """Leading dimension of a matrix that has x's shape, dtype and device (0 for None)."""
     if t is None:
         return 0
-    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
+    if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device():
         raise ValueError(f"{name} must have the shape {tuple(x.shape)}, dtype {x.dtype} and "
                          f"device {x.device} of x")
     return _matrix(t, name)[2]
@@ -355,16 +358,16 @@ def fp4q_quantize_mxfp8(x: torch.Tensor, e8m0_mode: int = E8M0_CEIL,
     """MXFP8 1x32 row-wise; returns {'q': [rows, cols] E4M3 codes, 'sf'}.  Any
     shape with cols % 32 == 0 may be swizzled (the padding is written as 0)."""
     rows, cols, ld = _matrix(x)
-    dev = x.device
+    index = x.get_device()
     n = _mx_scale_bytes(rows, cols, scale_layout)
     if out is None:
-        out = {"q": _u8((rows, cols), dev), "sf": _u8(n, dev)}
+        out = {"q": _u8((rows, cols), x.device), "sf": _u8(n, x.device)}
     else:
-        _expect(out["q"], "out['q']", (rows, cols), _U8, dev)
-        _expect_bytes(out["sf"], "out['sf']", n, dev)
+        _expect(out["q"], "out['q']", (rows, cols), _U8, index)
+        _expect_bytes(out["sf"], "out['sf']", n, index)
     _check("fp4q_quantize_mxfp8", lib().fp4q_quantize_mxfp8(
         x.data_ptr(), _dtype(x), rows, cols, ld, e8m0_mode, out["q"].data_ptr(),
-        out["sf"].data_ptr(), scale_layout, _raw_stream(dev)))
+        out["sf"].data_ptr(), scale_layout, _raw_stream(index)))
     return out
 
 
@@ -378,26 +381,26 @@ def fp4q_rmsnorm_mxfp8(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     ``out``, what it holds is written (want_y is not looked at)."""
     rows, cols, ld = _matrix(x)
     ld_res = _like(residual, x, "residual")
-    dev = x.device
-    _expect(weight, "weight", (cols,), _FLOATS, dev)
+    index = x.get_device()
+    _expect(weight, "weight", (cols,), _FLOATS, index)
     n = _mx_scale_bytes(rows, cols, scale_layout)
     if out is None:
-        out = {"q": _u8((rows, cols), dev), "sf": _u8(n, dev),
-               "rstd": torch.empty(rows, dtype=torch.float32, device=dev)}
+        out = {"q": _u8((rows, cols), x.device), "sf": _u8(n, x.device),
+               "rstd": torch.empty(rows, dtype=torch.float32, device=x.device)}
         if residual is not None:
-            out["sum"] = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+            out["sum"] = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
         if want_y:
-            out["y"] = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+            out["y"] = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
     else:
-        _expect(out["q"], "out['q']", (rows, cols), _U8, dev)
-        _expect_bytes(out["sf"], "out['sf']", n, dev)
-        _expect(out.get("rstd"), "out['rstd']", (rows,), _F32, dev)
-        _expect(out.get("sum"), "out['sum']", (rows, cols), (x.dtype,), dev)
-        _expect(out.get("y"), "out['y']", (rows, cols), (x.dtype,), dev)
+        _expect(out["q"], "out['q']", (rows, cols), _U8, index)
+        _expect_bytes(out["sf"], "out['sf']", n, index)
+        _expect(out.get("rstd"), "out['rstd']", (rows,), _F32, index)
+        _expect(out.get("sum"), "out['sum']", (rows, cols), (x.dtype,), index)
+        _expect(out.get("y"), "out['y']", (rows, cols), (x.dtype,), index)
     _check("fp4q_rmsnorm_mxfp8", lib().fp4q_rmsnorm_mxfp8(
         x.data_ptr(), _dtype(x), rows, cols, ld, _addr(residual), ld_res, weight.data_ptr(),
         _dtype(weight), eps, e8m0_mode, out["q"].data_ptr(), out["sf"].data_ptr(), scale_layout,
-        _addr(out.get("rstd")), _addr(out.get("sum")), _addr(out.get("y")), _raw_stream(dev)))
+        _addr(out.get("rstd")), _addr(out.get("sum")), _addr(out.get("y")), _raw_stream(index)))
     return out
 
 
@@ -410,24 +413,24 @@ def fp4q_rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     itself without a residual), dsum the gradient along the residual stream."""
     rows, cols, ld = _matrix(x)
     ld_dy, ld_dsum = _like(dy, x, "dy"), _like(dsum, x, "dsum")
-    dev = x.device
-    _expect(weight, "weight", (cols,), _FLOATS, dev)
-    _expect(rstd, "rstd", (rows,), _F32, dev)
+    index = x.get_device()
+    _expect(weight, "weight", (cols,), _FLOATS, index)
+    _expect(rstd, "rstd", (rows,), _F32, index)
     if out is None:
-        out = {"dx": torch.empty((rows, cols), dtype=x.dtype, device=dev),
-               "dweight": torch.empty(cols, dtype=torch.float32, device=dev)}
+        out = {"dx": torch.empty((rows, cols), dtype=x.dtype, device=x.device),
+               "dweight": torch.empty(cols, dtype=torch.float32, device=x.device)}
     else:
-        _expect(out["dx"], "out['dx']", (rows, cols), (x.dtype,), dev)
-        _expect(out["dweight"], "out['dweight']", (cols,), _F32, dev)
+        _expect(out["dx"], "out['dx']", (rows, cols), (x.dtype,), index)
+        _expect(out["dweight"], "out['dweight']", (cols,), _F32, index)
     need = lib().fp4q_rmsnorm_backward_workspace_bytes(rows, cols)
     if workspace is None:
-        workspace = _u8(need, dev)
+        workspace = _u8(need, x.device)
     else:
-        _expect_bytes(workspace, "workspace", need, dev)
+        _expect_bytes(workspace, "workspace", need, index)
     _check("fp4q_rmsnorm_backward", lib().fp4q_rmsnorm_backward(
         dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype(x), weight.data_ptr(), _dtype(weight),
         rstd.data_ptr(), _addr(dsum), ld_dsum, rows, cols, out["dx"].data_ptr(),
-        out["dweight"].data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(dev)))
+        out["dweight"].data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(index)))
     return out
 
 
@@ -498,21 +501,23 @@ def fp4q_gemm_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor, sfb: 
     return c
 
 
-def _matrix_out(out: torch.Tensor | None, rows: int, cols: int, dtype: torch.dtype, device
-                ) -> tuple[torch.Tensor, int, int]:
+def _matrix_out(out: torch.Tensor | None, rows: int, cols: int, dtype: torch.dtype,
+                like: torch.Tensor) -> tuple[torch.Tensor, int, int]:
     """The output matrix (a new one, or the caller's [rows, cols] with unit column
     stride), its dtype code and its leading dimension."""
     if out is None:
-        out = torch.empty((rows, cols), dtype=dtype, device=device)
-    elif out.device != device or tuple(out.shape) != (rows, cols):
-        raise ValueError(f"out must be a [{rows}, {cols}] tensor on {device}")
+        out = torch.empty((rows, cols), dtype=dtype, device=like.device)
+    elif out.get_device() != like.get_device() or out.shape != (rows, cols):
+        raise ValueError(f"out must be a [{rows}, {cols}] tensor on {like.device}")
     return out, _dtype(out), _matrix(out, "out")[2]
 
 
-def _status_addr(status: torch.Tensor | None, device):
-    if status is not None and (status.dtype != torch.int32 or status.device != device):
-        raise ValueError(f"status must be an int32 tensor on {device}")
-    return _addr(status)
+def _status_addr(status: torch.Tensor | None, index: int):
+    if status is None:
+        return None
+    if status.dtype != torch.int32 or status.get_device() != index:
+        raise ValueError(f"status must be an int32 tensor on cuda:{index}")
+    return status.data_ptr()
 
 
 def fp4q_gemm_mxfp8_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor,
@@ -526,16 +531,16 @@ def fp4q_gemm_mxfp8_mxfp4(qa: torch.Tensor, sfa: torch.Tensor, qb: torch.Tensor,
         raise ValueError("qa must be a CUDA tensor")
     if qa.dim() != 2 or qb.dim() != 2:
         raise ValueError("qa must be [M, K] and qb [N, K/2]")
-    (M, K), N, dev = qa.shape, qb.shape[0], qa.device
-    _expect(qa, "qa", (M, K), _U8, dev)
-    _expect(qb, "qb", (N, K // 2), _U8, dev)
+    (M, K), N, index = qa.shape, qb.shape[0], qa.get_device()
+    _expect(qa, "qa", (M, K), _U8, index)
+    _expect(qb, "qb", (N, K // 2), _U8, index)
     if K % 128 == 0:
-        _expect_bytes(sfa, "sfa", _mx_scale_bytes(M, K, SCALE_SWIZZLED), dev)
-        _expect_bytes(sfb, "sfb", _mx_scale_bytes(N, K, SCALE_SWIZZLED), dev)
-    c, cdt, ldc = _matrix_out(out, M, N, out_dtype, dev)
+        _expect_bytes(sfa, "sfa", _mx_scale_bytes(M, K, SCALE_SWIZZLED), index)
+        _expect_bytes(sfb, "sfb", _mx_scale_bytes(N, K, SCALE_SWIZZLED), index)
+    c, cdt, ldc = _matrix_out(out, M, N, out_dtype, qa)
     _check("fp4q_gemm_mxfp8_mxfp4", lib().fp4q_gemm_mxfp8_mxfp4(
         qa.data_ptr(), sfa.data_ptr(), qb.data_ptr(), sfb.data_ptr(), M, N, K, c.data_ptr(), cdt,
-        ldc, _status_addr(status, dev), _raw_stream(dev)))
+        ldc, _status_addr(status, index), _raw_stream(index)))
     return c
 
 
@@ -551,26 +556,26 @@ def fp4q_moe_mxfp4(xq: torch.Tensor, xsf: torch.Tensor, logits: torch.Tensor,
         raise ValueError("xq must be a CUDA tensor")
     if xq.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
         raise ValueError("xq must be [T, H], w13 [E, 2I, H/2] and w2 [E, H, I/2]")
-    (T, H), (E, I), dev = xq.shape, (w13.shape[0], w13.shape[1] // 2), xq.device
-    _expect(xq, "xq", (T, H), _U8, dev)
-    _expect(logits, "logits", (T, E), _FLOATS, dev)
-    _expect(w13, "w13", (E, 2 * I, H // 2), _U8, dev)
-    _expect(w2, "w2", (E, H, I // 2), _U8, dev)
+    (T, H), (E, I), index = xq.shape, (w13.shape[0], w13.shape[1] // 2), xq.get_device()
+    _expect(xq, "xq", (T, H), _U8, index)
+    _expect(logits, "logits", (T, E), _FLOATS, index)
+    _expect(w13, "w13", (E, 2 * I, H // 2), _U8, index)
+    _expect(w2, "w2", (E, H, I // 2), _U8, index)
     if H % 32 == 0 and I % 32 == 0:
-        _expect_bytes(xsf, "xsf", _mx_scale_bytes(T, H, SCALE_SWIZZLED), dev)
-        _expect_bytes(sf13, "sf13", _mx_scale_bytes(E * 2 * I, H, SCALE_SWIZZLED), dev)
-        _expect_bytes(sf2, "sf2", _mx_scale_bytes(E * H, I, SCALE_SWIZZLED), dev)
-    c, cdt, ldo = _matrix_out(out, T, H, out_dtype, dev)
+        _expect_bytes(xsf, "xsf", _mx_scale_bytes(T, H, SCALE_SWIZZLED), index)
+        _expect_bytes(sf13, "sf13", _mx_scale_bytes(E * 2 * I, H, SCALE_SWIZZLED), index)
+        _expect_bytes(sf2, "sf2", _mx_scale_bytes(E * H, I, SCALE_SWIZZLED), index)
+    c, cdt, ldo = _matrix_out(out, T, H, out_dtype, xq)
     need = lib().fp4q_moe_mxfp4_workspace_bytes(T, E, top_k, H, I)
     if workspace is None:
-        workspace = _u8(need, dev)
+        workspace = _u8(need, xq.device)
     else:
-        _expect_bytes(workspace, "workspace", need, dev)
+        _expect_bytes(workspace, "workspace", need, index)
     _check("fp4q_moe_mxfp4", lib().fp4q_moe_mxfp4(
         xq.data_ptr(), xsf.data_ptr(), logits.data_ptr(), _dtype(logits), w13.data_ptr(),
         sf13.data_ptr(), w2.data_ptr(), sf2.data_ptr(), T, E, top_k, H, I,
         int(bool(renormalize)), c.data_ptr(), cdt, ldo, workspace.data_ptr(), workspace.numel(),
-        _status_addr(status, dev), _raw_stream(dev)))
+        _status_addr(status, index), _raw_stream(index)))
     return c
 
 

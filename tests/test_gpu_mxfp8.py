@@ -86,3 +86,41 @@ def test_empty_and_another_stream():
         got = fq.fp4q_quantize_mxfp8(x)
     s.synchronize()
     assert torch.equal(got["q"], ref["q"]) and torch.equal(got["sf"], ref["sf"])
+
+
+def test_binding_refuses_what_does_not_fit():
+    """The Python calls' own checks: shapes, types, devices and densities of outputs."""
+    x = torch.zeros(4, 64, device=DEV)
+    w = torch.ones(64, device=DEV)
+    q, sf = torch.empty(4, 64, dtype=torch.uint8, device=DEV), torch.empty(8, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        fq.fp4q_quantize_mxfp8(x.cpu())
+    with pytest.raises(ValueError):
+        fq.fp4q_quantize_mxfp8(x.t())                    # columns without unit stride
+    with pytest.raises(TypeError):
+        fq.fp4q_quantize_mxfp8(x.half())
+    for bad in (q[:3], q.cpu(), torch.empty(4, 128, dtype=torch.uint8, device=DEV)[:, ::2]):
+        with pytest.raises(ValueError):
+            fq.fp4q_quantize_mxfp8(x, out={"q": bad, "sf": sf})
+    with pytest.raises(TypeError):
+        fq.fp4q_quantize_mxfp8(x, out={"q": q.view(torch.int8), "sf": sf})
+    with pytest.raises(ValueError):
+        fq.fp4q_quantize_mxfp8(x, out={"q": q, "sf": sf[:7]})
+    with pytest.raises(fq.Fp4qError):
+        fq.fp4q_quantize_mxfp8(torch.zeros(4, 48, device=DEV))
+    with pytest.raises(ValueError):
+        fq.fp4q_rmsnorm_mxfp8(x, w[:32])
+    with pytest.raises(ValueError):
+        fq.fp4q_rmsnorm_mxfp8(x, w, residual=x[:2])
+    with pytest.raises(ValueError):
+        fq.fp4q_rmsnorm_backward(x, x, w, torch.ones(3, device=DEV))
+    with pytest.raises(ValueError):
+        fq.fp4q_gemm_mxfp8_mxfp4(q, sf, q, sf)           # K of the weights
+    wq = torch.zeros(128, 64, dtype=torch.uint8, device=DEV)
+    xq = torch.zeros(4, 128, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError):
+        fq.fp4q_gemm_mxfp8_mxfp4(xq, sf, wq, torch.zeros(512, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        fq.fp4q_gemm_mxfp8_mxfp4(xq, torch.zeros(512, dtype=torch.uint8, device=DEV), wq,
+                                 torch.zeros(512, dtype=torch.uint8, device=DEV),
+                                 out=torch.empty(4, 64, device=DEV))
