@@ -118,10 +118,12 @@ __device__ __forceinline__ uint32_t ordered(float v) {
 // One token's choice by one warp: softmax statistics over E <= 32 NI logits (expert
 // lane + 32 i in register i), then k times the largest that is left.
 // An expert whose probability is 0 is not chosen; a row without a finite logit
-// chooses none.  e_sel, w_sel: [k] in shared memory; returns how many.
+// chooses none.  e_sel, w_sel: [k] in shared memory; sets the token's bit in the
+// masks of its experts; returns how many.
 template <int NI>
 __device__ __forceinline__ int choose(const void *logits, int dtype, int64_t row, int E, int k,
-                                      bool renormalize, int lane, int16_t *e_sel, float *w_sel) {
+                                      bool renormalize, int lane, int16_t *e_sel, float *w_sel,
+                                      unsigned long long *mask) {
   constexpr float kNone = -INFINITY;
   float v[NI];
   float top = kNone;
@@ -169,32 +171,56 @@ __device__ __forceinline__ int choose(const void *logits, int dtype, int64_t row
   if (lane < n) {
     e_sel[lane] = static_cast<int16_t>(mine_e);
     w_sel[lane] = renormalize ? __fdiv_rn(p, total) : p;
+    atomicOr(&mask[mine_e], 1ull << row);
   }
   return n;
 }
 
+// The chosen experts in shared memory, by active index.
+struct Chosen {
+  unsigned long long mask[kMoeMaxExperts];
+  int16_t expert[kMoeMaxExperts], offset[kMoeMaxExperts];
+  // From the table: all loads at once, `most` entries (those past n_active are not
+  // used), in place of a chain that waits for n_active first.  The caller's barrier
+  // follows.
+  __device__ __forceinline__ int load(const Table &tab, int most) {
+    const int n = *tab.n_active;
+    for (int a = threadIdx.x; a < most; a += blockDim.x) {
+      const int e = tab.expert[a], o = tab.offset[a];
+      const unsigned long long m = tab.mask[a];
+      expert[a] = static_cast<int16_t>(e);
+      offset[a] = static_cast<int16_t>(o);
+      mask[a] = m;
+    }
+    return n;
+  }
+};
+
 // The routing in shared memory.
 struct Routing {
   unsigned long long mask[kMoeMaxExperts];               // by expert: bit t, token t chose it
-  int16_t expert[kMoeMaxExperts], offset[kMoeMaxExperts];   // by active index
   int16_t first[kMoeMaxExperts];                         // offset by expert
   int16_t sel[kMoeMaxTokens * kMoeMaxTopK];              // a token's choices
   float wsel[kMoeMaxTokens * kMoeMaxTopK];
   int nsel[kMoeMaxTokens];
   int active;
+
+  // before route(), with a barrier between; needs nothing of the predecessor
+  __device__ __forceinline__ void clear(int E) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) mask[e] = 0;
+  }
 };
 
 // Worked out by all threads of a CTA, which ends with a barrier; `write` puts it
 // into the table.
-__device__ __forceinline__ void route(Routing &r, const void *logits, int logits_dtype, int T,
-                                      int E, int k, bool renormalize, bool write,
-                                      const Table &tab) {
+__device__ __forceinline__ void route(Routing &r, Chosen &ch, const void *logits,
+                                      int logits_dtype, int T, int E, int k, bool renormalize,
+                                      bool write, const Table &tab) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, threads = blockDim.x;
-  for (int e = threadIdx.x; e < E; e += threads) r.mask[e] = 0;
   auto choices = [&](auto ni) {
     for (int t = warp; t < T; t += threads / 32) {
       const int n = choose<decltype(ni)::value>(logits, logits_dtype, t, E, k, renormalize, lane,
-                                                r.sel + t * k, r.wsel + t * k);
+                                                r.sel + t * k, r.wsel + t * k, r.mask);
       if (lane == 0) r.nsel[t] = n;
     }
   };
@@ -204,14 +230,12 @@ __device__ __forceinline__ void route(Routing &r, const void *logits, int logits
   else if (E <= 128) choices(std::integral_constant<int, 4>{});
   else choices(std::integral_constant<int, 8>{});
   __syncthreads();
-  for (int i = threadIdx.x; i < T * k; i += threads)
-    if (i % k < r.nsel[i / k]) atomicOr(&r.mask[r.sel[i]], 1ull << (i / k));
-  __syncthreads();
   if (warp == 0) {
     int na = 0, no = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
       const int e = e0 + lane;
-      const int n = e < E ? __popcll(r.mask[e]) : 0;
+      const unsigned long long m = e < E ? r.mask[e] : 0;
+      const int n = __popcll(m);
       const uint32_t on = __ballot_sync(0xFFFFFFFFu, n > 0);
       int sc = n;                                         // inclusive scan of the counts
 #pragma unroll
@@ -221,8 +245,9 @@ __device__ __forceinline__ void route(Routing &r, const void *logits, int logits
       }
       if (n > 0) {
         const int a = na + __popc(on & ((1u << lane) - 1u));
-        r.expert[a] = static_cast<int16_t>(e);
-        r.offset[a] = r.first[e] = static_cast<int16_t>(no + sc - n);
+        ch.mask[a] = m;
+        ch.expert[a] = static_cast<int16_t>(e);
+        ch.offset[a] = r.first[e] = static_cast<int16_t>(no + sc - n);
       }
       na += __popc(on);
       no += __shfl_sync(0xFFFFFFFFu, sc, 31);
@@ -237,9 +262,9 @@ __device__ __forceinline__ void route(Routing &r, const void *logits, int logits
     tab.weight[r.first[e] + __popcll(r.mask[e] & ((1ull << t) - 1ull))] = r.wsel[i];
   }
   for (int a = threadIdx.x; a < r.active; a += threads) {
-    tab.expert[a] = r.expert[a];
-    tab.offset[a] = r.offset[a];
-    tab.mask[a] = r.mask[r.expert[a]];
+    tab.expert[a] = ch.expert[a];
+    tab.offset[a] = ch.offset[a];
+    tab.mask[a] = ch.mask[a];
   }
   if (threadIdx.x == 0) *tab.n_active = r.active;
 }
@@ -253,11 +278,14 @@ __global__ void __launch_bounds__(kRouteThreads)
 route_kernel(const uint8_t *xq, const uint8_t *xsf, const void *logits, int logits_dtype, int T,
              int E, int k, bool renormalize, int KT, Table tab) {
   __shared__ Routing r;
+  __shared__ Chosen ch;
   __shared__ int16_t s_active[kMoeMaxExperts];           // active index by expert
+  r.clear(E);
+  __syncthreads();
   begin_dependent();
-  route(r, logits, logits_dtype, T, E, k, renormalize, blockIdx.x == 0, tab);
+  route(r, ch, logits, logits_dtype, T, E, k, renormalize, blockIdx.x == 0, tab);
   for (int a = threadIdx.x; a < r.active; a += kRouteThreads)
-    s_active[r.expert[a]] = static_cast<int16_t>(a);
+    s_active[ch.expert[a]] = static_cast<int16_t>(a);
   __syncthreads();
   // per choice 8 KT chunks of 16 bytes and KT words of scales, all choices of the
   // CTA in one flat loop
@@ -280,21 +308,6 @@ route_kernel(const uint8_t *xq, const uint8_t *xsf, const void *logits, int logi
     }
   }
 }
-
-// The table in shared memory, for the kernels that read it.
-struct Chosen {
-  unsigned long long mask[kMoeMaxExperts];               // by active index
-  int16_t expert[kMoeMaxExperts], offset[kMoeMaxExperts];
-  __device__ __forceinline__ int load(const Table &tab) {   // the caller's barrier follows
-    const int n = *tab.n_active;
-    for (int a = threadIdx.x; a < n; a += blockDim.x) {
-      expert[a] = static_cast<int16_t>(tab.expert[a]);
-      offset[a] = static_cast<int16_t>(tab.offset[a]);
-      mask[a] = tab.mask[a];
-    }
-    return n;
-  }
-};
 
 // SORTED: x lies by expert in the table's buffers (map_x reads it in boxes of 16
 // rows); else map_x reads all T rows and the routing is worked out here.
@@ -331,23 +344,19 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     bars.init(2);
     *err_ptr = 0;
   }
-  begin_dependent_tma();
-  int n_active;
-  if constexpr (SORTED) {
-    n_active = ch.load(tab);
-  } else {
-    Routing &r = s_routing;
-    route(r, logits, logits_dtype, T, E, k, renormalize, blockIdx.x == 0, tab);
-    n_active = r.active;
-    for (int a = threadIdx.x; a < n_active; a += kThreads) {
-      ch.expert[a] = r.expert[a];
-      ch.offset[a] = r.offset[a];
-      ch.mask[a] = r.mask[r.expert[a]];
-    }
-  }
+  if constexpr (!SORTED) s_routing.clear(E);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  begin_dependent_tma();
+  int n_active;
+  if constexpr (SORTED) {
+    n_active = ch.load(tab, min(T * k, E));
+    __syncthreads();
+  } else {
+    route(s_routing, ch, logits, logits_dtype, T, E, k, renormalize, blockIdx.x == 0, tab);
+    n_active = s_routing.active;
+  }
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *slot_ptr, 0);
   const int n_units = n_active * NT;
 
@@ -532,8 +541,8 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
 template <typename OutT, int BN>
 __global__ void __launch_bounds__(kThreads, Down<BN>::PER_SM)
 down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
-            const uint8_t *sfw, Table tab, int T, int KT, int NT, int S, OutT *out, int64_t ldo,
-            int *status) {
+            const uint8_t *sfw, Table tab, int T, int E, int k, int KT, int NT, int S, OutT *out,
+            int64_t ldo, int *status) {
   using C = Down<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -560,15 +569,14 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
     bars.init(2);
     *err_ptr = 0;
   }
-  begin_dependent_tma();
-  const int n_active = ch.load(tab);
-  int rows = 0;                                           // rows of h
-  if (n_active > 0) rows = tab.offset[n_active - 1] + __popcll(tab.mask[n_active - 1]);
-  for (int i = threadIdx.x; i < rows; i += kThreads) s_weight[i] = tab.weight[i];
   for (int i = threadIdx.x; i < T * 128; i += kThreads) sum[i] = 0.0f;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  begin_dependent_tma();
+  const int n_active = ch.load(tab, min(T * k, E));
+  for (int i = threadIdx.x; i < T * k; i += kThreads) s_weight[i] = tab.weight[i];
+  __syncthreads();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *slot_ptr, 0);
   // this CTA's part of the list of (expert, K-tile), expert by expert
   const int total = n_active * KT;
@@ -762,7 +770,7 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   S = 1;
   while (S < 8 && tiles * S * 2 <= slots) S *= 2;
   return launch_dependent(k2, tiles * S, kThreads, Down<BN>::SMEM_BYTES, S, L, w2, h, m.sf2, tab,
-                          m.T, NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo, m.status);
+                          m.T, m.E, m.k, NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo, m.status);
 }
 
 }  // namespace
