@@ -76,9 +76,10 @@ template <int BN_, int STAGES_, int PER_SM_, int ACCS, int EXTRA> struct Stages 
 // the first product: two buffers of gate and up
 template <int BN>
 using GateUp = Stages<BN, BN == 64 ? 8 : BN == 32 ? 4 : 5, BN == 64 ? 1 : 2, 4, 0>;
-// the second: two accumulators, and the FP32 sums [BN][128]
-template <int BN>
-using Down = Stages<BN, BN == 64 ? 7 : 4, BN == 64 ? 1 : 2, 2, BN * 512>;
+// the second: two accumulators, and the FP32 sums [BN][128]; two CTAs an SM, or one
+// with a deep ring
+template <int BN, bool DEEP>
+using Down = Stages<BN, !DEEP ? 4 : BN == 64 ? 7 : 8, DEEP ? 1 : 2, 2, BN * 512>;
 
 // What a CTA's barriers and slots look like after its stages.
 template <int STAGES>
@@ -538,12 +539,12 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
                  : "memory");
 }
 
-template <typename OutT, int BN>
-__global__ void __launch_bounds__(kThreads, Down<BN>::PER_SM)
+template <typename OutT, int BN, bool DEEP>
+__global__ void __launch_bounds__(kThreads, Down<BN, DEEP>::PER_SM)
 down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
             const uint8_t *sfw, Table tab, int T, int E, int k, int KT, int NT, int S, OutT *out,
             int64_t ldo, int *status) {
-  using C = Down<BN>;
+  using C = Down<BN, DEEP>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Chosen ch;
@@ -728,17 +729,17 @@ struct Layout {
   }
 };
 
-template <typename OutT, int BN>
+template <typename OutT, int BN, bool DEEP>
 cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   static KernelSetup setup1, setup2;
   int per_sm = 0;
   constexpr bool kSorted = BN > 16;
   auto *k1 = gate_up_kernel<BN, kSorted>;
-  auto *k2 = down_kernel<OutT, BN>;
+  auto *k2 = down_kernel<OutT, BN, DEEP>;
   cudaError_t e = kernel_setup(setup1, reinterpret_cast<const void *>(k1), kThreads,
                                GateUp<BN>::SMEM_BYTES, &per_sm);
   if (e != cudaSuccess) return e;
-  e = kernel_setup(setup2, reinterpret_cast<const void *>(k2), kThreads, Down<BN>::SMEM_BYTES,
+  e = kernel_setup(setup2, reinterpret_cast<const void *>(k2), kThreads, Down<BN, DEEP>::SMEM_BYTES,
                    &per_sm);
   if (e != cudaSuccess) return e;
   const int KT1 = static_cast<int>(m.H / 128), NT1 = static_cast<int>(m.I / 128);
@@ -766,10 +767,10 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   if (e != cudaSuccess) return e;
   // second product: the largest cluster that leaves every cluster its place
   const int64_t tiles = m.H / 128;
-  slots = static_cast<int64_t>(L.num_sms) * Down<BN>::PER_SM;
+  slots = static_cast<int64_t>(L.num_sms) * Down<BN, DEEP>::PER_SM;
   S = 1;
   while (S < 8 && tiles * S * 2 <= slots) S *= 2;
-  return launch_dependent(k2, tiles * S, kThreads, Down<BN>::SMEM_BYTES, S, L, w2, h, m.sf2, tab,
+  return launch_dependent(k2, tiles * S, kThreads, Down<BN, DEEP>::SMEM_BYTES, S, L, w2, h, m.sf2, tab,
                           m.T, m.E, m.k, NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo, m.status);
 }
 
@@ -794,9 +795,16 @@ cudaError_t launch_moe_mxfp4(const MoeArgs &m, void *workspace, const Launch &L)
   tab.hsf = ws + at.hsf;
   auto go = [&](auto o) {
     using O = decltype(o);
-    if (m.T <= 16) return launch_t<O, 16>(m, tab, L);
-    if (m.T <= 32) return launch_t<O, 32>(m, tab, L);
-    return launch_t<O, 64>(m, tab, L);
+    if (m.T <= 16) return launch_t<O, 16, false>(m, tab, L);
+    if (m.T > 32) return launch_t<O, 64, true>(m, tab, L);
+    // between, a deep ring pays where an SM has much to read (32 tokens, 64 experts,
+    // 4096 x 2048, 256 K-tiles an SM: 161 us against 175); with little, two CTAs of
+    // which the first can start while the first product's last one drains (16 experts,
+    // 2048 x 1024, 16 K-tiles: 30 us against 37)
+    const int64_t most = m.T * m.k < m.E ? m.T * m.k : m.E;
+    if (most * (m.I / 128) * (m.H / 128) >= 96 * static_cast<int64_t>(L.num_sms))
+      return launch_t<O, 32, true>(m, tab, L);
+    return launch_t<O, 32, false>(m, tab, L);
   };
   return m.out_dtype == FP4Q_BF16 ? go(__nv_bfloat16{}) : go(float{});
 }

@@ -186,3 +186,49 @@ def test_norm_router_and_layer_captured():
     torch.cuda.synchronize()
     for o, e, (_, _, ref) in zip(outs, eager, want):
         assert torch.equal(o, ref) and torch.equal(e, ref)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(20, 16, 4, 4096, 3584), (64, 24, 6, 2048, 4096),
+                                       (1, 8, 8, 8192, 2048), (16, 12, 3, 4096, 2048)])
+def test_large_layers(T, E, k, H, I):
+    """Sizes at which the kernels take their deep rings, against FP64 products on the
+    GPU of the operands as fp4q_dequantize (tested bit for bit) gives them.  Tolerance as
+    above; h's moved codes are the root of a row's worst case."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+
+    def w4(rows, cols):
+        q = torch.randint(0, 256, (rows, cols // 2), dtype=torch.uint8, device=DEV, generator=g)
+        s = torch.randint(119, 122, (rows * cols // 32,), dtype=torch.uint8, device=DEV, generator=g)
+        return q, s
+
+    (q13, s13), (q2, s2) = w4(E * 2 * I, H), w4(E * H, I)
+    xq = fq.fp4q_quantize_mxfp8(torch.randn(T, H, device=DEV, generator=g),
+                                scale_layout=fq.SCALE_SWIZZLED)
+    logits = torch.randn(T, E, device=DEV, generator=g)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = fq.fp4q_moe_mxfp4(xq["q"], xq["sf"], logits, q13.view(E, 2 * I, H // 2), s13,
+                            q2.view(E, H, I // 2), s2, top_k=k, out_dtype=torch.float32,
+                            status=status)
+    assert int(status) == 0
+    p = torch.from_numpy(plain.route(logits.double().cpu().numpy(), k, True)).to(DEV)
+
+    def read(q, s, rows, cols, fmt=fq.FMT_MXFP4):
+        return fq.fp4q_dequantize(fmt, q, s, rows, cols, 1, 32,
+                                  scale_layout=fq.SCALE_SWIZZLED).double()
+
+    x = read(xq["q"], xq["sf"], T, H, fq.FMT_MXFP8)
+    want, mag, flip = (torch.zeros(T, H, dtype=torch.float64, device=DEV) for _ in range(3))
+    for e in range(E):
+        w = read(q13.view(E, -1)[e], s13.view(E, -1)[e], 2 * I, H)
+        a = x @ w.t()
+        h = a[:, :I] / (1 + torch.exp(-a[:, :I])) * a[:, I:]
+        v, ex = plain.quantize(h.cpu().numpy())
+        h = torch.from_numpy(v * np.repeat(np.ldexp(1.0, ex), 32, 1)).to(DEV)
+        w = read(q2.view(E, -1)[e], s2.view(E, -1)[e], H, I)
+        want += p[:, e:e + 1] * (h @ w.t())
+        mag += p[:, e:e + 1] * (h.abs() @ w.abs().t())
+        flip = torch.maximum(flip, p[:, e:e + 1] * h.abs().amax(1, keepdim=True) * w.abs().max())
+    err = (got.double() - want).abs()
+    bound = 4 * (H + I + E + 64) * 2.0 ** -22 * mag + 2 * flip * 2.0 ** -3
+    assert bool((err <= bound).all())
+    assert float((got.double() - want).norm() / want.norm()) < 1e-3
