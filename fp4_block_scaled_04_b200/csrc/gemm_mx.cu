@@ -265,7 +265,7 @@ cudaError_t launch_t(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw, c
 // and the MMA (M = 256, issued by the leader) reads both halves of the tokens.
 // A CTA alone is bound by shared-memory traffic (96 KB per K-tile of 128 x 256 x
 // 128: 362 us at 8192 x 14336 x 4096, 25.0 at 333 x 4096 x 14336); in pairs it
-// falls by a third, and so does the traffic from L2 (336 and 22.0 us).
+// falls by a third, and so does the traffic from L2 (331 and 22.4 us).
 struct Pair {
   static constexpr int STAGES = 6;
   static constexpr int W_BYTES = 128 * 128, W_TX = W_BYTES / 2;
@@ -588,7 +588,8 @@ cudaError_t launch_pair(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw
       !make_map_scales(&map_sfw, sfw, N / 128 * p.KT) ||
       !make_map_scales(&map_sfx, sfx, (M + 127) / 128 * p.KT))
     return cudaErrorInvalidValue;
-  const int64_t units = static_cast<int64_t>(p.nt_m) * p.nt_n, places = pair_clusters<OutT>(2 * p.S);
+  const int64_t units = static_cast<int64_t>(p.nt_m) * p.nt_n;
+  const int64_t places = pair_clusters<OutT>(2 * p.S);
   const int64_t clusters = p.S > 1 || units < places ? units : places;
   return launch_dependent(kern, clusters * 2 * p.S, kThreads, Pair::SMEM_BYTES, 2 * p.S, L, map_w,
                           map_x, map_sfw, map_sfx, M, N, p, static_cast<OutT *>(c), ldc, status);

@@ -1,5 +1,5 @@
 // moe.cu -- a whole mixture-of-experts layer with MXFP4 weights for a few
-// tokens (T <= 64), in two kernels.
+// tokens (T <= 64), in two kernels (above 16 tokens in three).
 //
 //   p = softmax(logits), the k largest (ties: the lowest index), optionally
 //   renormalized to sum 1; for every chosen expert e of a token
@@ -316,8 +316,8 @@ template <int BN, bool SORTED>
 __global__ void __launch_bounds__(kThreads, GateUp<BN>::PER_SM)
 gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
                const __grid_constant__ CUtensorMap map_x, const uint8_t *sfw, const uint8_t *sfx,
-               const void *logits, int logits_dtype, int T, int E, int k, bool renormalize, int KT, int NT, int S, Table tab,
-               int *status) {
+               const void *logits, int logits_dtype, int T, int E, int k, bool renormalize, int KT,
+               int NT, int S, Table tab, int *status) {
   using C = GateUp<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -739,13 +739,13 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   cudaError_t e = kernel_setup(setup1, reinterpret_cast<const void *>(k1), kThreads,
                                GateUp<BN>::SMEM_BYTES, &per_sm);
   if (e != cudaSuccess) return e;
-  e = kernel_setup(setup2, reinterpret_cast<const void *>(k2), kThreads, Down<BN, DEEP>::SMEM_BYTES,
-                   &per_sm);
+  e = kernel_setup(setup2, reinterpret_cast<const void *>(k2), kThreads,
+                   Down<BN, DEEP>::SMEM_BYTES, &per_sm);
   if (e != cudaSuccess) return e;
   const int KT1 = static_cast<int>(m.H / 128), NT1 = static_cast<int>(m.I / 128);
   CUtensorMap w13, w2, x, h;
   if (!make_map_mxfp4(&w13, m.w13, m.E * 2 * m.I, m.H) ||
-      !make_map_mxfp4(&w2, m.w2, m.E * m.H, m.I) || 
+      !make_map_mxfp4(&w2, m.w2, m.E * m.H, m.I) ||
       !make_map_mxfp8(&x, kSorted ? tab.xq : m.xq, kSorted ? m.T * m.k : m.T, m.H, 16) ||
       !make_map_mxfp8(&h, tab.hq, m.T * m.k, m.I, 16))
     return cudaErrorInvalidValue;
@@ -770,8 +770,9 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   slots = static_cast<int64_t>(L.num_sms) * Down<BN, DEEP>::PER_SM;
   S = 1;
   while (S < 8 && tiles * S * 2 <= slots) S *= 2;
-  return launch_dependent(k2, tiles * S, kThreads, Down<BN, DEEP>::SMEM_BYTES, S, L, w2, h, m.sf2, tab,
-                          m.T, m.E, m.k, NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo, m.status);
+  return launch_dependent(k2, tiles * S, kThreads, Down<BN, DEEP>::SMEM_BYTES, S, L, w2, h, m.sf2,
+                          tab, m.T, m.E, m.k, NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo,
+                          m.status);
 }
 
 }  // namespace

@@ -396,7 +396,8 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s, int
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
   const int n8 = cols / 8;
   const int row_bytes = cols * static_cast<int>(sizeof(T)), tensors = dsum ? 3 : 2;
-  float *dw = reinterpret_cast<float *>(ring + static_cast<size_t>(RING ? depth : 0) * tensors * G * row_bytes);
+  float *dw = reinterpret_cast<float *>(ring + static_cast<size_t>(RING ? depth : 0) * tensors *
+                                                  G * row_bytes);
   // this row's part, in two planes of float4 as the ring's
   uint8_t *mine = reinterpret_cast<uint8_t *>(dw + grp * cols);
 #pragma unroll

@@ -9,7 +9,9 @@ is computed once, then the kernel under study runs ``--warmup`` times and
 ``--iters`` times more, with a device synchronize at the end.  Each of those
 runs is exactly one launch of the kernel named by ``--op`` (the amax
 pre-pass is outside them; ``gemm_if4`` launches the IF4 split pass before
-its GEMM), so a profiler can skip the warm-up launches and capture the rest.
+its GEMM, ``norm_backward`` the sum of dweight after it, the expert layers two
+kernels or three), so a profiler can skip the warm-up launches and capture the
+rest.
 """
 from __future__ import annotations
 
@@ -24,7 +26,8 @@ from fp4_block_scaled_04_b200 import workloads
 OPS = ["amax", "nvfp4_row", "nvfp4_rowcol", "mxfp4_rowcol", "2d", "rht16_sr", "rht128_sr",
        "rht16_rne", "rht128_rne", "if4", "if4_dequant", "four_over_six_rowcol", "nvint4",
        "bwd16_sr", "bwd16_rne", "row_sr", "mxfp6_e2m3", "mxfp6_dequant", "gemm_nvfp4", "gemm_if4", "if6", "if3",
-       "if3_dequant"]
+       "if3_dequant", "mxfp8", "mxfp8_dequant", "norm", "norm_backward", "gemm_mxfp8", "gemm_mxfp8_one",
+       "moe_one", "moe_64"]
 
 
 def make(op: str, rows: int, cols: int, dev):
@@ -69,6 +72,46 @@ def make(op: str, rows: int, cols: int, dev):
         return lambda: fq.fp4q_gemm_if4_nvfp4(ox["q"], ox["sf"], ow["q_row"], ow["sf_row"], cols,
                                               tensor_scale_a=ox["s_dec"],
                                               tensor_scale_b=ow["s_dec"], out=c, workspace=ws)
+    if op in ("mxfp8", "mxfp8_dequant", "norm", "norm_backward"):
+        x = workloads.activation(rows=rows, cols=cols).to(dev)
+        if op.startswith("norm"):
+            w = torch.linspace(0.5, 1.5, cols, device=dev).to(torch.bfloat16)
+            r = x.flip(0).contiguous()
+            o = fq.fp4q_rmsnorm_mxfp8(x, w, residual=r, scale_layout=sw)
+            if op == "norm":
+                return lambda: fq.fp4q_rmsnorm_mxfp8(x, w, residual=r, scale_layout=sw, out=o)
+            ob = fq.fp4q_rmsnorm_backward(x, o["sum"], w, o["rstd"], dsum=r)
+            return lambda: fq.fp4q_rmsnorm_backward(x, o["sum"], w, o["rstd"], dsum=r, out=ob)
+        o = fq.fp4q_quantize_mxfp8(x, scale_layout=sw)
+        if op == "mxfp8":
+            return lambda: fq.fp4q_quantize_mxfp8(x, scale_layout=sw, out=o)
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+        return lambda: fq.fp4q_dequantize(fq.FMT_MXFP8, o["q"], o["sf"], rows, cols, 1, 32,
+                                          scale_layout=sw, out=y)
+    if op in ("gemm_mxfp8", "gemm_mxfp8_one"):   # N = rows, K = cols; M = rows, or one token
+        g = torch.Generator(device=dev).manual_seed(7)
+        m = 1 if op.endswith("one") else rows
+        x = torch.randn(m, cols, device=dev, generator=g)
+        w = torch.randn(rows, cols, device=dev, generator=g) * 0.05
+        ox = fq.fp4q_quantize_mxfp8(x, scale_layout=fq.SCALE_SWIZZLED)
+        ow = fq.fp4q_quantize_mxfp4(w, scale_layout=fq.SCALE_SWIZZLED)
+        c = torch.empty((m, rows), dtype=torch.bfloat16, device=dev)
+        return lambda: fq.fp4q_gemm_mxfp8_mxfp4(ox["q"], ox["sf"], ow["q_row"], ow["sf_row"], out=c)
+    if op in ("moe_one", "moe_64"):     # 16 experts, hidden size rows, expert width cols
+        g = torch.Generator(device=dev).manual_seed(8)
+        t, e = (1, 16) if op == "moe_one" else (64, 16)
+        x = fq.fp4q_quantize_mxfp8(torch.randn(t, rows, device=dev, generator=g),
+                                   scale_layout=fq.SCALE_SWIZZLED)
+        logits = torch.randn(t, e, device=dev, generator=g)
+
+        def w4(n, k):
+            o = fq.fp4q_quantize_mxfp4(torch.randn(n, k, device=dev, generator=g) * 0.05,
+                                       scale_layout=fq.SCALE_SWIZZLED)
+            return o["q_row"], o["sf_row"]
+
+        (q13, s13), (q2, s2) = w4(e * 2 * cols, rows), w4(e * rows, cols)
+        q13, q2 = q13.view(e, 2 * cols, rows // 2), q2.view(e, rows, cols // 2)
+        return lambda: fq.fp4q_moe_mxfp4(x["q"], x["sf"], logits, q13, s13, q2, s2, top_k=4)
     if op in ("mxfp6_e2m3", "mxfp6_dequant"):
         x = workloads.activation(rows=rows, cols=cols).to(dev)
         o = fq.fp4q_quantize_mxfp6(x, fq.FP6_E2M3, scale_layout=sw)

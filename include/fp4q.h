@@ -589,7 +589,7 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const u
  *          are chosen (ties: the lowest index) and, with renormalize != 0,
  *          divided by their sum.  -inf masks an expert (NaN counts as -inf);
  *          an expert of probability 0 is not chosen, so that a row without a
- *          finite logit chooses none and its output is 0
+ *          finite logit, or with one of +inf, chooses none and its output is 0
  *   a    = x W13_e^T in FP32;  h = MXFP8(silu(a[gate]) * a[up]), rounded as
  *          fp4q_quantize_mxfp8 with FP4Q_E8M0_CEIL
  *   out  = RN(sum over the chosen experts, in index order, of p_e (h W2_e^T))
