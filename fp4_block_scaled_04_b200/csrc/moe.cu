@@ -131,7 +131,8 @@ __device__ __forceinline__ int choose(const void *logits, int dtype, int64_t row
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int e = lane + 32 * i;
-    v[i] = e < E ? load_logit(logits, dtype, row * E + e) : kNone;
+    // + 0: -0 becomes 0, which ties with it
+    v[i] = e < E ? __fadd_rn(load_logit(logits, dtype, row * E + e), 0.0f) : kNone;
     if (!(v[i] > kNone)) v[i] = kNone;                   // NaN counts as masked
     top = fmaxf(top, v[i]);
   }

@@ -114,6 +114,19 @@ def test_masks_ties_and_bf16_logits():
             check(got, L, x, t, 4, renorm)
 
 
+@pytest.mark.parametrize("T", [3, 20])
+def test_zeros_of_either_sign_tie(T):
+    """-0 and 0 are equal logits: the lowest indices are chosen, whatever the signs."""
+    L = Layer(40, 256, 256, 13)
+    xq, x = tokens(T, 256, 14)
+    logits = torch.zeros(T, 40)
+    logits[:, :24] = -0.0
+    logits[1, 3::7] = 0.0
+    for t in (logits.to(DEV), logits.bfloat16().to(DEV)):
+        got = fq.fp4q_moe_mxfp4(xq["q"], xq["sf"], t, *L.dev, top_k=4, out_dtype=torch.float32)
+        check(got, L, x, t, 4, True)
+
+
 def test_equals_the_librarys_products():
     """One expert, one token choice of weight 1: the layer is product, activation,
     quantizer and product, bit for bit where the first product's sums agree."""
