@@ -117,7 +117,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
   const float e = __fmaf_rn(-__fmul_rn(v, r), r, 1.0f);
-  return v > 0.0f ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
+  // at 0 and inf (squares that pass FP32) the step would make NaN of inf and 0
+  return v > 0.0f && v < INFINITY ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
 }
 
 // max(m, |a|, |b|)

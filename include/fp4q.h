@@ -370,7 +370,8 @@ fp4q_status fp4q_quantize_mxfp8(const void *x, int dtype, int64_t rows, int64_t 
  * producer of the activation in front of a block-scaled product.  Per row of H
  * = cols values, in FP32:
  *   s    = RN_T(x + residual), or x without a residual (T the dtype of x)
- *   rstd = 1 / sqrt(mean(s^2) + eps)          (the mean in the kernel's order)
+ *   rstd = 1 / sqrt(mean(s^2) + eps)          (the mean in the kernel's order; 0
+ *          where the sum of squares passes FP32)
  *   y    = RN(RN(s * rstd) * weight)
  *   q, sf  MXFP8 of y, as fp4q_quantize_mxfp8 (y itself is not rounded first)
  *   x, residual  [rows, cols] of dtype, leading dimensions ld, ld_residual;

@@ -109,6 +109,24 @@ def test_zero_rows_of_values_and_eps():
     check_forward(out, x, w, 1e-6, False)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("rows,cols", [(3, 96), (300, 1056)])
+def test_squares_past_fp32(rows, cols, dtype):
+    """A row whose squares pass FP32 has rstd 0 and normed values of 0; its
+    neighbours are what they are without it."""
+    x = matrix(rows, cols, 31, dtype).contiguous()
+    w = matrix(1, cols, 32, BF16)[0]
+    want = fq.fp4q_rmsnorm_mxfp8(x, w, want_y=True)
+    x[1] = 1e25
+    got = fq.fp4q_rmsnorm_mxfp8(x, w, want_y=True)
+    others = [i for i in range(rows) if i != 1]
+    for k in ("q", "y", "rstd"):
+        assert torch.equal(got[k][others], want[k][others])
+        assert not got[k][1].float().any() or k == "q"
+    assert not (got["q"][1] & 0x7F).any()
+    assert not got["sf"].view(rows, -1)[1].any()
+
+
 def test_strided_inputs_in_place_sum_and_empty():
     x, r = matrix(33, 640, 7, BF16, ld=704), matrix(33, 640, 8, BF16, ld=1024)
     w = matrix(1, 640, 9, BF16)[0]
