@@ -16,12 +16,33 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// 32 values.  Plain loads here and below, and no pointer that promises data that
+// stays unchanged: the kernels begin while their predecessor may still write what
+// they read, so a load may neither go the read-only way nor before the wait.
+__device__ __forceinline__ void load32(const __nv_bfloat16 *p, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+    v[8 * i + 0] = bf16_lo(u.x); v[8 * i + 1] = bf16_hi(u.x);
+    v[8 * i + 2] = bf16_lo(u.y); v[8 * i + 3] = bf16_hi(u.y);
+    v[8 * i + 4] = bf16_lo(u.z); v[8 * i + 5] = bf16_hi(u.z);
+    v[8 * i + 6] = bf16_lo(u.w); v[8 * i + 7] = bf16_hi(u.w);
+  }
+}
+__device__ __forceinline__ void load32(const float *p, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float4 f = reinterpret_cast<const float4 *>(p)[i];
+    v[4 * i + 0] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+  }
+}
+
 // One thread per 32-value block, over the scale matrix as it is written (the
 // padding of the swizzled layout included: a zero byte and no codes).
 template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads)
-mxfp8_kernel(const T *__restrict__ x, I rows, I cols, I ld, int mode, uint8_t *__restrict__ q,
-             uint8_t *__restrict__ sf, int scale_layout, I srows, I scols) {
+mxfp8_kernel(const T *x, I rows, I cols, I ld, int mode, uint8_t *q, uint8_t *sf,
+             int scale_layout, I srows, I scols) {
   begin_dependent();
   const I bpr = cols / 32, nblk = srows * scols;
   const I stride = static_cast<I>(gridDim.x) * kThreads;
@@ -33,7 +54,7 @@ mxfp8_kernel(const T *__restrict__ x, I rows, I cols, I ld, int mode, uint8_t *_
       continue;
     }
     float v[32];
-    load_values<32, T>(x + r * ld + cb * 32, v);
+    load32(x + r * ld + cb * 32, v);
     float m = 0.0f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) m = fmaxf(m, fabsf(v[k]));
@@ -59,16 +80,16 @@ mxfp8_kernel(const T *__restrict__ x, I rows, I cols, I ld, int mode, uint8_t *_
 // FP32 rounding (it only rounds below the normal range).
 template <typename OutT, typename I>
 __global__ void __launch_bounds__(kThreads)
-mxfp8_dequant_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ sf,
-                     int scale_layout, I rows, I cols, OutT *__restrict__ y) {
+mxfp8_dequant_kernel(const uint8_t *q, const uint8_t *sf, int scale_layout, I rows, I cols,
+                     OutT *y) {
   begin_dependent();
   const I upr = cols / 8, n = rows * upr;
   const I scols = static_cast<I>(scale_cols(cols / 32, scale_layout));
   const I stride = static_cast<I>(gridDim.x) * kThreads;
   for (I u = static_cast<I>(blockIdx.x) * kThreads + threadIdx.x; u < n; u += stride) {
     const I r = u / upr, cb = (u - r * upr) / 4;
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q) + u);
-    const float p = e8m0_value(__ldg(sf + scale_offset_t<I>(r, cb, scols, scale_layout)));
+    const uint2 w = reinterpret_cast<const uint2 *>(q)[u];
+    const float p = e8m0_value(sf[scale_offset_t<I>(r, cb, scols, scale_layout)]);
     float2 v[4];
     const uint32_t half[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
 #pragma unroll

@@ -150,6 +150,10 @@ __device__ __forceinline__ float row_sum(float v, float *slot, int warp) {
   return t;
 }
 
+// (No __restrict__ on these kernels' pointers: they begin while their predecessor
+// may still write what they read, and the word would let a load go the read-only
+// way, or before the wait.)
+//
 // W warps share a row; a CTA holds max(W, 4) warps, so G = 1, 2 or 4 rows at a
 // time, and walks the groups of rows blockIdx.x, + gridDim.x, ...  A thread keeps
 // up to VPT vectors of 8 values in registers: vector lane + 32 (warp in row) +
@@ -161,9 +165,8 @@ __device__ __forceinline__ float row_sum(float v, float *slot, int warp) {
 template <typename T, typename TW, int W, int VPT, bool RING, bool FULL>
 __global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
 rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int64_t ld_res,
-               const TW *__restrict__ weight, float eps, int mode, uint8_t *__restrict__ q,
-               uint8_t *__restrict__ sf, int scale_layout, float *__restrict__ rstd_out,
-               T *sum_out, T *__restrict__ y_out, int depth) {
+               const TW *weight, float eps, int mode, uint8_t *q, uint8_t *sf, int scale_layout,
+               float *rstd_out, T *sum_out, T *y_out, int depth) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
   extern __shared__ __align__(16) uint8_t ring[];        // [depth][x, residual][G] rows
   __shared__ __align__(16) float slot[2][NW];
@@ -386,10 +389,9 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
 // alternate between loading and computing).
 template <typename T, typename TW, int W, int VPT, bool RING>
 __global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
-rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *__restrict__ s, int64_t ld_s,
-                        const TW *__restrict__ weight, const float *__restrict__ rstd,
-                        const T *dsum, int64_t ld_dsum, int64_t rows, int cols, T *dx,
-                        float *__restrict__ part, int depth) {
+rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, const TW *weight,
+                        const float *rstd, const T *dsum, int64_t ld_dsum, int64_t rows, int cols,
+                        T *dx, float *part, int depth) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
   extern __shared__ __align__(16) uint8_t ring[];        // [depth][dy, s, dsum][G] rows, [G] dw
   __shared__ __align__(16) float slot[2][NW];
