@@ -127,6 +127,22 @@ def test_squares_past_fp32(rows, cols, dtype):
     assert not got["sf"].view(rows, -1)[1].any()
 
 
+@pytest.mark.parametrize("rows,cols", [(3, 96), (300, 1056)])
+def test_large_weights_and_values(rows, cols):
+    """Weights whose product with x would pass FP32 although y does not; a row at the
+    type's largest value."""
+    x = (matrix(rows, cols, 33, BF16).float() * 2.0 ** 40).to(BF16)
+    w = matrix(1, cols, 34, BF16)[0].clone()
+    w[5::11] = 2.0 ** 100
+    check_forward(fq.fp4q_rmsnorm_mxfp8(x, w), x, w, 1e-6, False)
+    x[2] = torch.finfo(BF16).max
+    w[5::11] = 3.0
+    out = fq.fp4q_rmsnorm_mxfp8(x, w, want_y=True)
+    assert float(out["rstd"][2]) == 0 and not out["y"][2].float().any()
+    keep = [i for i in range(rows) if i != 2]
+    assert torch.isfinite(out["y"][keep].float()).all()
+
+
 def test_strided_inputs_in_place_sum_and_empty():
     x, r = matrix(33, 640, 7, BF16, ld=704), matrix(33, 640, 8, BF16, ld=1024)
     w = matrix(1, 640, 9, BF16)[0]
