@@ -87,22 +87,38 @@ template <> struct Raw8<float> {
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// A ring of rows in shared memory, filled by cp.async.  A thread copies the
-// vectors that it reads itself, so that it needs no barrier, only its own
-// groups' completion.  A row's 16-byte pieces lie plane by plane (an FP32 vector
-// of 8 values has two), so that neighbouring lanes use neighbouring banks.
-template <typename T>
-__device__ __forceinline__ void ring_copy(uint32_t row, const T *p, int v8, int n8) {
+// A ring of rows in shared memory, filled by cp.async in pieces of 16 bytes and laid
+// out as in memory.  Neighbouring lanes copy neighbouring pieces (on both sides:
+// with the halves of FP32 vectors in planes of their own, whichever side is
+// scattered, 8192 x 4096 took 109 us forward and 143 backward).  BF16: a thread
+// copies the vectors that it reads itself and needs only its own groups' completion.
+// FP32: a vector is two pieces and a warp copies its 32 vectors together, with a
+// warp barrier (ring_sync) before it reads and before the next copies.
+// fn(offset of this lane's piece in the row) for each piece of its vector v8.
+template <typename T, bool FULL, typename F>
+__device__ __forceinline__ void ring_pieces(int v8, int n8, int lane, F fn) {
+  if constexpr (sizeof(T) == 2) {
+    if (FULL || v8 < n8) fn(16 * v8);
+  } else {
 #pragma unroll
-  for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
-    cp_async16(row + (h * n8 + v8) * 16, reinterpret_cast<const uint8_t *>(p) + 16 * h);
+    for (int h = 0; h < 2; ++h) {
+      const int piece = 2 * (v8 - lane) + 32 * h + lane;
+      if (FULL || piece < 2 * n8) fn(16 * piece);
+    }
+  }
 }
 template <typename T>
-__device__ __forceinline__ Raw8<T> ring_get(const uint8_t *row, int v8, int n8) {
+__device__ __forceinline__ void ring_copy(uint32_t row, const T *p, int at) {
+  cp_async16(row + at, reinterpret_cast<const uint8_t *>(p) + at);
+}
+template <typename T>
+__device__ __forceinline__ void ring_sync() {
+  if constexpr (sizeof(T) == 4) __syncwarp();
+}
+template <typename T>
+__device__ __forceinline__ Raw8<T> ring_get(const uint8_t *row, int v8) {
   Raw8<T> r;
-#pragma unroll
-  for (int h = 0; h < static_cast<int>(sizeof(T)) / 2; ++h)
-    reinterpret_cast<uint4 *>(&r)[h] = *reinterpret_cast<const uint4 *>(row + (h * n8 + v8) * 16);
+  r.load(reinterpret_cast<const T *>(row) + 8 * v8);
   return r;
 }
 
@@ -197,12 +213,10 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
     if (row < rows) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int v8 = lane + 32 * (wr + W * j);
-        if (mine(v8)) {
-          ring_copy(smem_u32(ring) + place(stage, 0), x + row * ld + 8 * v8, v8, n8);
-          if (res)
-            ring_copy(smem_u32(ring) + place(stage, 1), res + row * ld_res + 8 * v8, v8, n8);
-        }
+        ring_pieces<T, FULL>(lane + 32 * (wr + W * j), n8, lane, [&](int at) {
+          ring_copy(smem_u32(ring) + place(stage, 0), x + row * ld, at);
+          if (res) ring_copy(smem_u32(ring) + place(stage, 1), res + row * ld_res, at);
+        });
       }
     }
     cp_async_commit();
@@ -225,9 +239,11 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
     const int64_t e0 = row * cols;
     uint8_t *const sf_at = sf + sf_row(row);
     if constexpr (RING) {
+      ring_sync<T>();
       fetch(stage == 0 ? depth - 1 : stage - 1, row + (depth - 1) * step);
       if (depth == 3) cp_async_wait<2>();
       else cp_async_wait<1>();
+      ring_sync<T>();
     }
     Raw8<T> s[VPT];
     float2 ss = both(0.0f);
@@ -237,8 +253,8 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
       if (live && mine(v8)) {
         Raw8<T> rr;
         if constexpr (RING) {
-          s[j] = ring_get<T>(ring + place(stage, 0), v8, n8);
-          if (res) rr = ring_get<T>(ring + place(stage, 1), v8, n8);
+          s[j] = ring_get<T>(ring + place(stage, 0), v8);
+          if (res) rr = ring_get<T>(ring + place(stage, 1), v8);
         } else {
           s[j].load(x + row * ld + 8 * v8);
           if (res) rr.load(res + row * ld_res + 8 * v8);
@@ -308,8 +324,9 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
 // The depth of a ring of groups of `bytes` each next to `fixed` bytes: 3 or 2
 // where two CTAs then fit an SM, else 3 or 2 for one (rows of 20 KB: 2 deep and two
 // CTAs beat 3 deep and one), else none.
+constexpr int64_t kTwoCtas = 112 * 1024;
 inline int ring_depth(int64_t bytes, int64_t fixed) {
-  for (const int64_t room : {112 * 1024, 220 * 1024})
+  for (const int64_t room : {kTwoCtas, int64_t{220 * 1024}})
     for (int d = 3; d >= 2; --d)
       if (d * bytes + fixed <= room) return d;
   return 0;
@@ -353,8 +370,10 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
   constexpr integral_constant<int, 3> three{};
   constexpr integral_constant<int, 4> four{};
   constexpr integral_constant<int, 5> five{};
-  // Few rows: each on as many warps as it has vectors, no ring.
-  if (rows <= L.num_sms && n8 <= 1024) {
+  // Few rows: each on as many warps as it has vectors, no ring.  Narrow ones up to
+  // eight an SM (1184 x 1024 BF16: 4.2 us, 4.3 with the ring; 300 x 1024: 2.4 and 3.1;
+  // FP32 700 x 992: 3.5 and 4.8), wide ones up to one (300 x 4096: 6.1 and 4.5).
+  if (n8 <= 1024 && rows <= L.num_sms * (n8 <= 128 ? 8 : 1)) {
     if (n8 <= 32) return run(one, one, false_type{}, false_type{});
     if (n8 <= 128) return run(four, one, false_type{}, false_type{});
     if (n8 <= 512) return run(integral_constant<int, 16>{}, one, false_type{}, false_type{});
@@ -374,7 +393,9 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
   if (n8 <= 160) return go(one);
   if (n8 <= 320) return go(integral_constant<int, 2>{});
   if (n8 <= 640) return go(four);
-  if (n8 <= 1280) return go(integral_constant<int, 8>{});
+  // while two CTAs fit an SM (see ring_depth); one has more warps
+  const int64_t pair = 2 * (res ? 2 : 1) * cols * static_cast<int64_t>(sizeof(T));
+  if (n8 <= 1280 && (pair <= kTwoCtas || sizeof(T) == 2)) return go(integral_constant<int, 8>{});
   if (ring_depth((res ? 2 : 1) * cols * static_cast<int64_t>(sizeof(T)), 0) == 0)
     return run(integral_constant<int, 32>{}, four, false_type{}, false_type{});
   if (n8 <= 2560) return go(integral_constant<int, 16>{});
@@ -401,7 +422,7 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, co
   const int row_bytes = cols * static_cast<int>(sizeof(T)), tensors = dsum ? 3 : 2;
   float *dw = reinterpret_cast<float *>(ring + static_cast<size_t>(RING ? depth : 0) * tensors *
                                                   G * row_bytes);
-  // this row's part, in two planes of float4 as the ring's
+  // this row's part, in two planes of float4 (neighbouring lanes on neighbouring banks)
   uint8_t *mine = reinterpret_cast<uint8_t *>(dw + grp * cols);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -417,13 +438,11 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, co
     if (row < rows) {
 #pragma unroll
       for (int j = 0; j < VPT; ++j) {
-        const int v8 = lane + 32 * (wr + W * j);
-        if (v8 < n8) {
-          ring_copy(smem_u32(ring) + place(stage, 0), dy + row * ld_dy + 8 * v8, v8, n8);
-          ring_copy(smem_u32(ring) + place(stage, 1), s + row * ld_s + 8 * v8, v8, n8);
-          if (dsum)
-            ring_copy(smem_u32(ring) + place(stage, 2), dsum + row * ld_dsum + 8 * v8, v8, n8);
-        }
+        ring_pieces<T, false>(lane + 32 * (wr + W * j), n8, lane, [&](int at) {
+          ring_copy(smem_u32(ring) + place(stage, 0), dy + row * ld_dy, at);
+          ring_copy(smem_u32(ring) + place(stage, 1), s + row * ld_s, at);
+          if (dsum) ring_copy(smem_u32(ring) + place(stage, 2), dsum + row * ld_dsum, at);
+        });
       }
     }
     cp_async_commit();
@@ -445,9 +464,11 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, co
     const bool live = row < rows;
     const float r = live ? rstd[row] : 0.0f;
     if constexpr (RING) {
+      ring_sync<T>();
       fetch(stage == 0 ? depth - 1 : stage - 1, row + (depth - 1) * step);
       if (depth == 3) cp_async_wait<2>();
       else cp_async_wait<1>();
+      ring_sync<T>();
     }
     Raw8<T> gv[VPT], sv[VPT], dv[VPT];
 #pragma unroll
@@ -455,9 +476,9 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, co
       const int v8 = lane + 32 * (wr + W * j);
       if (live && v8 < n8) {
         if constexpr (RING) {
-          gv[j] = ring_get<T>(ring + place(stage, 0), v8, n8);
-          sv[j] = ring_get<T>(ring + place(stage, 1), v8, n8);
-          if (dsum) dv[j] = ring_get<T>(ring + place(stage, 2), v8, n8);
+          gv[j] = ring_get<T>(ring + place(stage, 0), v8);
+          sv[j] = ring_get<T>(ring + place(stage, 1), v8);
+          if (dsum) dv[j] = ring_get<T>(ring + place(stage, 2), v8);
         } else {
           gv[j].load(dy + row * ld_dy + 8 * v8);
           sv[j].load(s + row * ld_s + 8 * v8);
@@ -474,7 +495,9 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, co
         gv[j].get(g);
         sv[j].get(x);
         wv[j].get(w);
-        Raw8<float> a = ring_get<float>(mine, v8, n8);
+        Raw8<float> a;
+        a.a = *reinterpret_cast<const float4 *>(mine + v8 * 16);
+        a.b = *reinterpret_cast<const float4 *>(mine + (n8 + v8) * 16);
         a.get(acc);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -598,9 +621,13 @@ cudaError_t launch_bwd(const void *dy, int64_t ld_dy, const void *s, int64_t ld_
   if (n8 <= 96) return go(integral_constant<int, 1>{});
   if (n8 <= 192) return go(two);
   if (n8 <= 384) return go(integral_constant<int, 4>{});
-  if (n8 <= 768) return go(integral_constant<int, 8>{});
-  const int64_t row = cols * static_cast<int64_t>(sizeof(T));
-  if (ring_depth((dsum ? 3 : 2) * row, cols * 4) == 0) {
+  // eight warps while two CTAs fit an SM, sixteen in one (8192 x 5120 FP32 with dsum:
+  // 111 us, 135 on eight)
+  const int64_t row = cols * static_cast<int64_t>(sizeof(T)), group = (dsum ? 3 : 2) * row;
+  if (n8 <= 768 && 2 * group + cols * 4 <= kTwoCtas) return go(integral_constant<int, 8>{});
+  if (ring_depth(group, cols * 4) == 0) {
+    // (4096 x 8192 FP32: 97 us on 16 warps, 134 on 32, whose 64 registers a thread spill)
+    if (n8 <= 1024) return run(integral_constant<int, 16>{}, two, std::false_type{});
     if (n8 <= 2048) return run(integral_constant<int, 32>{}, two, std::false_type{});
     return run(integral_constant<int, 32>{}, integral_constant<int, 4>{}, std::false_type{});
   }

@@ -187,6 +187,27 @@ def test_backward(rows, cols, dtype, wdtype):
         assert torch.equal(got["dx"], again["dx"]) and torch.equal(got["dweight"], again["dweight"])
 
 
+@pytest.mark.parametrize("dtype,wdtype", [(BF16, BF16), (BF16, FP32), (FP32, FP32), (FP32, BF16)])
+@pytest.mark.parametrize("rows,cols", [(149, 32), (301, 512), (1190, 1024), (1185, 1056),
+                                       (1184, 992), (330, 2080), (300, 4096), (599, 5120),
+                                       (301, 6144), (150, 6176), (300, 8192), (149, 10240),
+                                       (150, 12320)])
+def test_many_rows(rows, cols, dtype, wdtype):
+    """Both passes with a residual, at widths on either side of the forms' borders and
+    at more rows than the GPU takes at once."""
+    x, r = matrix(rows, cols, 51, dtype), matrix(rows, cols, 52, dtype)
+    g = matrix(rows, cols, 53, dtype, 0.1)
+    w = (1 + 0.2 * matrix(1, cols, 54, FP32)[0]).to(wdtype)
+    out = fq.fp4q_rmsnorm_mxfp8(x, w, residual=r, scale_layout=fq.SCALE_SWIZZLED)
+    s = (x.float() + r.float()).to(dtype)
+    assert torch.equal(out["sum"], s)
+    check_forward(out, s, w, 1e-6, True)
+    got = fq.fp4q_rmsnorm_backward(g, s, w, out["rstd"], dsum=r)
+    check_backward(got, g, s, w, out["rstd"], r, dtype)
+    check_forward(fq.fp4q_rmsnorm_mxfp8(s, w), s, w, 1e-6, False)
+    check_backward(fq.fp4q_rmsnorm_backward(g, s, w, out["rstd"]), g, s, w, out["rstd"], None, dtype)
+
+
 def test_backward_strided_in_place_and_empty():
     s, g = matrix(50, 640, 15, BF16, ld=768), matrix(50, 640, 16, BF16, 1e-2, ld=648)
     d = matrix(50, 640, 17, BF16, 1e-2, ld=1280)
