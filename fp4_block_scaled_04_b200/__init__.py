@@ -347,10 +347,14 @@ def _like(t: torch.Tensor | None, x: torch.Tensor, name: str) -> int:
     """Leading dimension of a matrix that has x's shape, dtype and device (0 for None)."""
     if t is None:
         return 0
-    if t.shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device():
+    shape = t.shape
+    if shape != x.shape or t.dtype != x.dtype or t.get_device() != x.get_device():
         raise ValueError(f"{name} must have the shape {tuple(x.shape)}, dtype {x.dtype} and "
                          f"device {x.device} of x")
-    return _matrix(t, name)[2]
+    ld, step = t.stride()
+    if step != 1:
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
+    return ld if shape[0] > 1 else shape[1]
 
 
 def fp4q_quantize_mxfp8(x: torch.Tensor, e8m0_mode: int = E8M0_CEIL,
@@ -422,15 +426,16 @@ def fp4q_rmsnorm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     else:
         _expect(out["dx"], "out['dx']", (rows, cols), (x.dtype,), index)
         _expect(out["dweight"], "out['dweight']", (cols,), _F32, index)
-    need = lib().fp4q_rmsnorm_backward_workspace_bytes(rows, cols)
+    L = lib()
+    need = L.fp4q_rmsnorm_backward_workspace_bytes(rows, cols)
     if workspace is None:
         workspace = _u8(need, x.device)
     else:
         _expect_bytes(workspace, "workspace", need, index)
-    _check("fp4q_rmsnorm_backward", lib().fp4q_rmsnorm_backward(
+    _check("fp4q_rmsnorm_backward", L.fp4q_rmsnorm_backward(
         dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype(x), weight.data_ptr(), _dtype(weight),
         rstd.data_ptr(), _addr(dsum), ld_dsum, rows, cols, out["dx"].data_ptr(),
-        out["dweight"].data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(index)))
+        out["dweight"].data_ptr(), workspace.data_ptr(), need, _raw_stream(index)))
     return out
 
 
