@@ -176,7 +176,7 @@ __device__ __forceinline__ float row_sum(float v, float *slot, int warp) {
 // 32 W j, so a warp's loads are contiguous and the 4 lanes of a 32-value block are
 // neighbours.  RING: `depth` (2 or 3) groups in shared memory keep loads in
 // flight through the reduction and the stores (8192 x 4096 BF16 with a residual:
-// 39 us, 5.99 TB/s; 53 without it).  Rows too wide for it are loaded directly
+// 40 us, 5.9 TB/s; 53 without it).  Rows too wide for it are loaded directly
 // instead.
 template <typename T, typename TW, int W, int VPT, bool RING, bool FULL>
 __global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
@@ -380,7 +380,7 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
     return run(integral_constant<int, 32>{}, one, false_type{}, false_type{});
   }
   // Many: three to five vectors a thread, which spread the work that each row costs
-  // once over the most values (8192 x 4096 BF16: 39.4 us on four warps, 41.7 on
+  // once over the most values (8192 x 4096 BF16: 40 us on four warps, 42 on
   // eight, 55 on two).
   auto go = [&](auto w) {
     constexpr int W = decltype(w)::value;
