@@ -153,12 +153,12 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _dtype(x: torch.Tensor) -> int:
+def _dtype(x: torch.Tensor, name: str = "input") -> int:
     if x.dtype == torch.bfloat16:
         return _BF16
     if x.dtype == torch.float32:
         return _FP32
-    raise TypeError(f"input must be bfloat16 or float32, got {x.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float32, got {x.dtype}")
 
 
 def _matrix(x: torch.Tensor, name: str = "x"):
@@ -336,6 +336,18 @@ def _expect_bytes(t: torch.Tensor, name: str, n: int, index: int) -> None:
     if t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     raise ValueError(f"{name} must be a contiguous uint8 tensor of at least {n} bytes")
+
+
+def _expect_room(t: torch.Tensor, name: str, n: int, index: int, itemsize: int = 0) -> None:
+    """A dense tensor of at least n elements (of itemsize bytes, where one is given) on
+    this CUDA device, whatever its shape."""
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    if itemsize and t.element_size() != itemsize:
+        raise TypeError(f"{name} must have elements of {itemsize} bytes, got {t.dtype}")
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of at least {n} elements, got "
+                         f"shape {tuple(t.shape)}, strides {t.stride()}")
 
 
 _U8 = (torch.uint8,)
@@ -752,11 +764,18 @@ def fp4q_dequantize(fmt: int, q: torch.Tensor, sf: torch.Tensor, rows: int, cols
                     out_dtype: torch.dtype = torch.float32,
                     out: torch.Tensor | None = None) -> torch.Tensor:
     """Packed codes ([rows, cols/2]; [rows, cols*3/4] for MXFP6 and IF6; [rows,
-    cols*3/8] for IF3) + scales -> [rows, cols] in out_dtype (fp32 or bf16)."""
+    cols*3/8] for IF3; [rows, cols] for MXFP8) + scales -> [rows, cols] in
+    out_dtype (fp32 or bf16).  MXFP8's swizzled scales are padded to whole
+    128x4 tiles, so a buffer of the other layout has another size."""
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
+    index = q.get_device()
     y = torch.empty((rows, cols), dtype=out_dtype, device=q.device) if out is None else out
-    ydt = _BF16 if y.dtype == torch.bfloat16 else _FP32
+    ydt = _dtype(y, "out")
+    _expect_room(y, "out", rows * cols, index)
+    if fmt == FMT_MXFP8:
+        _expect_room(q, "q", rows * cols, index, 1)
+        _expect_room(sf, "sf", _mx_scale_bytes(rows, cols, scale_layout), index, 1)
     _check("fp4q_dequantize", lib().fp4q_dequantize(
         fmt, _ptr(q), _ptr(sf), scale_layout, block_rows, block_cols, _ptr(tensor_scale), rows,
         cols, _ptr(y), ydt, _stream(q.device)))
