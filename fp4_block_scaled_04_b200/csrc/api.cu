@@ -3,6 +3,7 @@
 // Each entry point checks its arguments on the host (returning a status and
 // enqueueing nothing on error), makes the device that owns the input current,
 // and enqueues its kernels on the caller's stream.
+#include <climits>
 #include <cstdint>
 #include <cstring>
 #include <initializer_list>
@@ -862,10 +863,23 @@ fp4q_status fp4q_rmsnorm_backward(const void *dy, int64_t ld_dy, const void *x, 
                                              static_cast<float *>(workspace), L));
 }
 
-fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
-                                  const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
-                                  int c_dtype, int64_t ldc, int *status, void *stream) {
-  DeviceGuard guard;
+}  // extern "C"
+
+namespace fp4q {
+namespace {
+// The test hooks' waits: about 10 ms, and loaders that stop after some K-tiles.
+Waits withheld(int64_t loads0, int64_t loads1) {
+  Waits w;
+  w.cycles = 20000000;
+  w.stop0 = static_cast<int>(loads0 < INT_MAX ? loads0 : INT_MAX);
+  w.stop1 = static_cast<int>(loads1 < INT_MAX ? loads1 : INT_MAX);
+  return w;
+}
+
+fp4q_status gemm_mx_checked(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
+                            const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
+                            int c_dtype, int64_t ldc, int *status, const Waits &waits,
+                            void *stream) {
   if (!valid_dtype(c_dtype)) return FP4Q_ERR_INVALID_ARG;
   if (M < 0 || N < 0 || K < 0 || ldc < N) return FP4Q_ERR_INVALID_ARG;
   if (N % 128 != 0 || K % 128 != 0) return FP4Q_ERR_UNSUPPORTED_SHAPE;
@@ -894,7 +908,29 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const u
   FP4Q_TRY(check_dev(sfb, false));
   FP4Q_TRY(check_dev(status, true));
   return cuda_status(
-      launch_gemm_mxfp8_mxfp4(qa, sfa, qb, sfb, M, N, K, c, c_dtype, ldc, status, L));
+      launch_gemm_mxfp8_mxfp4(qa, sfa, qb, sfb, M, N, K, c, c_dtype, ldc, status, waits, L));
+}
+}  // namespace
+}  // namespace fp4q
+
+extern "C" {
+
+fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
+                                  const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
+                                  int c_dtype, int64_t ldc, int *status, void *stream) {
+  DeviceGuard guard;
+  return gemm_mx_checked(qa, sfa, qb, sfb, M, N, K, c, c_dtype, ldc, status, Waits{}, stream);
+}
+
+fp4q_status fp4q_gemm_mxfp8_mxfp4_withhold_loads(const uint8_t *qa, const uint8_t *sfa,
+                                                 const uint8_t *qb, const uint8_t *sfb, int64_t M,
+                                                 int64_t N, int64_t K, void *c, int c_dtype,
+                                                 int64_t ldc, int64_t loads0, int64_t loads1,
+                                                 int *status, void *stream) {
+  DeviceGuard guard;
+  if (!status || K == 0 || loads0 < 0 || loads1 < 0) return FP4Q_ERR_INVALID_ARG;
+  return gemm_mx_checked(qa, sfa, qb, sfb, M, N, K, c, c_dtype, ldc, status,
+                         withheld(loads0, loads1), stream);
 }
 
 size_t fp4q_moe_mxfp4_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64_t H, int64_t I) {

@@ -69,7 +69,7 @@ template <typename OutT, typename T>
 __global__ void __launch_bounds__(kThreads, T::PER_SM)
 gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
                const __grid_constant__ CUtensorMap map_x, const uint8_t *sfw, const uint8_t *sfx,
-               int M, const Plan plan, OutT *c, int64_t ldc, int *status) {
+               int M, const Plan plan, OutT *c, int64_t ldc, int *status, const Waits waits) {
   constexpr int STAGES = T::STAGES;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -114,15 +114,15 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *slot_ptr, 0);
   begin_dependent_tma();
+  int issued = 0;                                         // the loading warp's K-tiles
 
   if (warp == 0) {
     Ring<STAGES> ring(1);                                 // the first round finds it empty
-    int issued = 0;
     bool ok = true;
     for (int u = cl; u < n_units && ok; u += ncl) {
       const uint8_t *fw = sfw + static_cast<int64_t>(u) * KT * 512;
-      for (int kt = k0; kt < k1; ++kt, ++issued) {
-        if (!warp_wait(empty + 8 * ring.s, ring.phase)) {
+      for (int kt = k0; kt < k1 && issued != waits.stop0; ++kt, ++issued) {
+        if (!warp_wait(empty + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
         }
@@ -139,10 +139,7 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
       }
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
-    if (!ok) {
-      *err_ptr = 1;
-      drain_loads<STAGES>(full, issued);
-    }
+    if (!ok) *err_ptr = 1;
   } else if (warp == 1) {
     Ring<STAGES> ring(0);
     int b = 0;                                            // accumulator and its phase
@@ -152,13 +149,13 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
     const uint64_t dsf = desc_sf(base + T::SF_OFF);
     constexpr uint32_t idesc = idesc_mx4x8(BN);
     for (int u = cl; u < n_units && ok; u += ncl) {
-      if (!warp_wait(acc_empty + 8 * b, bphase)) {
+      if (!warp_wait(acc_empty + 8 * b, bphase, waits.cycles)) {
         ok = false;
         break;
       }
       tc_fence_after();
       for (int kt = k0; kt < k1; ++kt) {
-        if (!warp_wait(full + 8 * ring.s, ring.phase)) {
+        if (!warp_wait(full + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
         }
@@ -178,19 +175,14 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
       if (b == 0) bphase ^= 1;
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
-    if (!ok) {                                            // wait for the MMAs in flight
-      *err_ptr = 1;
-      if (elect_one()) tc_commit(drain);
-      __syncwarp();
-      warp_wait(drain, 0);
-    }
+    if (!ok) *err_ptr = 1;
   } else {
     const int quarter = warp & 3, row = quarter * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     int b = 0;
     uint32_t bphase = 0;
     for (int u = cl; u < n_units; u += ncl) {
-      if (!warp_wait(acc_full + 8 * b, bphase)) {
+      if (!warp_wait(acc_full + 8 * b, bphase, waits.cycles)) {
         *err_ptr = 1;
         break;
       }
@@ -227,7 +219,19 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && status && *err_ptr) atomicExch(status, 1);
+  if (*err_ptr) {
+    // a wait ran out: the CTA's MMAs and copies come to their end before it does
+    if (threadIdx.x == 0 && status) atomicExch(status, 1);
+    if (warp == 1) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      warp_wait(drain, 0, waits.cycles);
+    } else if (warp == 0) {
+      drain_loads<STAGES>(full, issued, waits.cycles);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(T::TMEM_COLS)
@@ -237,7 +241,7 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
 template <typename OutT, typename T>
 cudaError_t launch_t(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw, const uint8_t *sfw,
                      int64_t M, int64_t N, int64_t K, void *c, int64_t ldc, int *status,
-                     const Launch &L) {
+                     const Waits &waits, const Launch &L) {
   static KernelSetup setup;
   int per_sm = 0;
   auto *kern = gemm_mx_kernel<OutT, T>;
@@ -257,7 +261,7 @@ cudaError_t launch_t(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw, c
   while (plan.S < 8 && units * plan.S * 2 <= slots && plan.KT >= 4 * plan.S) plan.S *= 2;
   const int64_t grid = plan.S > 1 ? units * plan.S : units < slots ? units : slots;
   return launch_dependent(kern, grid, kThreads, T::SMEM_BYTES, plan.S, L, map_w, map_x, sfw, sfx,
-                          M, plan, static_cast<OutT *>(c), ldc, status);
+                          M, plan, static_cast<OutT *>(c), ldc, status, waits);
 }
 
 // Many tokens: the pair form.  Two CTAs share a tile of 256 weight rows x `cols`
@@ -282,7 +286,7 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
                     const __grid_constant__ CUtensorMap map_x,
                     const __grid_constant__ CUtensorMap map_sfw,
                     const __grid_constant__ CUtensorMap map_sfx, int M, int N, const Plan plan,
-                    OutT *c, int64_t ldc, int *status) {
+                    OutT *c, int64_t ldc, int *status, const Waits waits) {
   using T = Pair;
   constexpr int STAGES = T::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -290,9 +294,10 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
   const uint32_t full = base + STAGES * T::STAGE_BYTES, empty = full + 8 * STAGES;
   const uint32_t acc_full = empty + 8 * STAGES, acc_empty = acc_full + 16;
   const uint32_t drain = acc_empty + 16;
-  const uint32_t tmem_slot = drain + 8, err_slot = tmem_slot + 4;
+  const uint32_t tmem_slot = drain + 8, err_slot = tmem_slot + 4, issued_slot = err_slot + 4;
   volatile uint32_t *slot_ptr = reinterpret_cast<volatile uint32_t *>(smem_raw + (tmem_slot - raw));
   volatile int *err_ptr = reinterpret_cast<volatile int *>(smem_raw + (err_slot - raw));
+  volatile int *issued_ptr = reinterpret_cast<volatile int *>(smem_raw + (issued_slot - raw));
   float *part = reinterpret_cast<float *>(smem_raw + (base - raw));   // [cols][128], after the MMAs
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int cols = plan.cols, nacc = plan.nacc, KT = plan.KT, S = plan.S;
@@ -303,6 +308,13 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
   const int n_units = plan.nt_m * plan.nt_n;
   const int k0 = static_cast<int>(static_cast<int64_t>(KT) * p / S);
   const int k1 = static_cast<int>(static_cast<int64_t>(KT) * (p + 1) / S);
+  // the bytes that one CTA loads a stage
+  const uint32_t bytes = T::W_TX + cols / 2 * 128 + 3 * 512;
+  // a wait ran out: all CTAs of the cluster learn of it (by their first barrier below
+  // at the latest), since the end of one depends on the others'
+  auto raise = [&] {
+    if (lane < 2 * S) peer_store(peer_smem(err_slot, lane), 1);
+  };
 
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -336,20 +348,20 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
     int issued = 0;
     bool ok = true;
     const uint32_t leader_full = peer_smem(full, leader);
-    const uint32_t bytes = 2 * (T::W_TX + cols / 2 * 128 + 3 * 512);
+    const int stop = half == 0 ? waits.stop0 : waits.stop1;
     for (int u = cl; u < n_units && ok; u += ncl) {
       int mt, nt;
       tile_of(u, plan.nt_m, plan.nt_n, &mt, &nt);
       const int wt = 2 * nt + static_cast<int>(half);     // this CTA's weight tile
       const int m0 = mt * cols, x0 = m0 + static_cast<int>(half) * (cols / 2);
-      for (int kt = k0; kt < k1; ++kt, ++issued) {
-        if (!warp_wait_cluster(empty + 8 * ring.s, ring.phase)) {
+      for (int kt = k0; kt < k1 && issued != stop; ++kt, ++issued) {
+        if (!warp_wait_cluster(empty + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
         }
         const uint32_t st = base + ring.s * T::STAGE_BYTES, bar = leader_full + 8 * ring.s;
         if (elect_one()) {
-          if (half == 0) mbar_expect_tx(full + 8 * ring.s, bytes);
+          if (half == 0) mbar_expect_tx(full + 8 * ring.s, 2 * bytes);
           tma_load_2d_pair(st, &map_w, kt * 128, wt * 128, bar);
           tma_load_2d_pair(st + T::W_BYTES, &map_x, kt * 128, x0, bar);
           tma_load_2d_pair(st + T::SF_OFF, &map_sfw, 0, 2 * (wt * KT + kt), bar);
@@ -362,14 +374,8 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
       }
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
-    if (!ok) {
-      // no copy is in flight when the CTAs end: the leader sees both CTAs' bytes
-      // land; the other, whose barrier that is not, gives its last ones 0.1 ms
-      *err_ptr = 1;
-      if (half == 0) drain_loads<STAGES>(full, issued);
-      for (const long long t0 = clock64(); clock64() - t0 < 200000;) {}
-      __syncwarp();
-    }
+    if (!ok) raise();
+    if (lane == 0) *issued_ptr = issued;
   } else if (warp == 1) {
     if (half == 0) {
       Ring<STAGES> ring(0);
@@ -381,7 +387,7 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
       // M = 256: bits 24-28 hold M / 16
       const uint32_t idesc = (idesc_mx4x8(cols) & ~(31u << 24)) | (16u << 24);
       for (int u = cl; u < n_units && ok; u += ncl) {
-        if (!warp_wait_cluster(acc_empty + 8 * b, bphase)) {
+        if (!warp_wait_cluster(acc_empty + 8 * b, bphase, waits.cycles)) {
           ok = false;
           break;
         }
@@ -392,7 +398,7 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         tile_of(u, plan.nt_m, plan.nt_n, &mt, &nt);
         const uint32_t skip = mt * cols % 128 / 32;
         for (int kt = k0; kt < k1; ++kt) {
-          if (!warp_wait_cluster(full + 8 * ring.s, ring.phase)) {
+          if (!warp_wait_cluster(full + 8 * ring.s, ring.phase, waits.cycles)) {
             ok = false;
             break;
           }
@@ -413,12 +419,7 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
         }
         ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
       }
-      if (!ok) {                                          // wait for the MMAs in flight
-        *err_ptr = 1;
-        if (elect_one()) tc_commit_pair(drain, leader);
-        __syncwarp();
-        warp_wait_cluster(drain, 0);
-      }
+      if (!ok) raise();
     }
   } else {
     const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -427,8 +428,8 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
     int b = 0;
     uint32_t bphase = 0;
     for (int u = cl; u < n_units; u += ncl) {
-      if (!warp_wait_cluster(acc_full + 8 * b, bphase)) {
-        *err_ptr = 1;
+      if (!warp_wait_cluster(acc_full + 8 * b, bphase, waits.cycles)) {
+        raise();
         break;
       }
       tc_fence_after();
@@ -498,7 +499,21 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
   }
   __syncwarp();
   cluster_sync();                                         // all MMAs and parts are complete
-  if (S > 1) {
+  if (*err_ptr) {
+    // or a wait ran out, in which case every CTA of the cluster is here, and the pair's
+    // MMAs and copies come to their end before either CTA does
+    if (threadIdx.x == 0 && status) atomicExch(status, 1);
+    if (warp == 1) {
+      if (half == 0 && elect_one()) tc_commit_pair(drain, leader);
+      __syncwarp();
+      warp_wait_cluster(drain, 0, waits.cycles);
+    } else if (warp == 0 && half == 0) {
+      const int other = static_cast<int>(peer_load_u32(peer_smem(issued_slot, leader + 1)));
+      drain_loads_pair<STAGES>(full, *issued_ptr, other, bytes, waits.cycles);
+    }
+    __syncwarp();
+    cluster_sync();
+  } else if (S > 1) {
     int mt, nt;
     tile_of(cl, plan.nt_m, plan.nt_n, &mt, &nt);
     const int n0 = nt * 256 + static_cast<int>(half) * 128;
@@ -509,7 +524,6 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && status && *err_ptr) atomicExch(status, 1);
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
@@ -554,7 +568,7 @@ int pair_clusters(int size) {
 template <typename OutT>
 cudaError_t launch_pair(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw,
                         const uint8_t *sfw, int64_t M, int64_t N, int64_t K, void *c, int64_t ldc,
-                        int *status, const Launch &L) {
+                        int *status, const Waits &waits, const Launch &L) {
   static KernelSetup setup;
   int per_sm = 0;
   auto *kern = gemm_mx_pair_kernel<OutT>;
@@ -592,28 +606,30 @@ cudaError_t launch_pair(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw
   const int64_t places = pair_clusters<OutT>(2 * p.S);
   const int64_t clusters = p.S > 1 || units < places ? units : places;
   return launch_dependent(kern, clusters * 2 * p.S, kThreads, Pair::SMEM_BYTES, 2 * p.S, L, map_w,
-                          map_x, map_sfw, map_sfx, M, N, p, static_cast<OutT *>(c), ldc, status);
+                          map_x, map_sfw, map_sfx, M, N, p, static_cast<OutT *>(c), ldc, status,
+                          waits);
 }
 
 template <typename OutT>
 cudaError_t launch_o(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw, const uint8_t *sfw,
                      int64_t M, int64_t N, int64_t K, void *c, int64_t ldc, int *status,
-                     const Launch &L) {
+                     const Waits &waits, const Launch &L) {
   if (M <= 16)
-    return launch_t<OutT, Cfg<16, 5, 2>>(qx, sfx, qw, sfw, M, N, K, c, ldc, status, L);
+    return launch_t<OutT, Cfg<16, 5, 2>>(qx, sfx, qw, sfw, M, N, K, c, ldc, status, waits, L);
   if (M <= 64)
-    return launch_t<OutT, Cfg<64, 4, 2>>(qx, sfx, qw, sfw, M, N, K, c, ldc, status, L);
-  return launch_pair<OutT>(qx, sfx, qw, sfw, M, N, K, c, ldc, status, L);
+    return launch_t<OutT, Cfg<64, 4, 2>>(qx, sfx, qw, sfw, M, N, K, c, ldc, status, waits, L);
+  return launch_pair<OutT>(qx, sfx, qw, sfw, M, N, K, c, ldc, status, waits, L);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
                                     const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
-                                    int c_dtype, int64_t ldc, int *status, const Launch &L) {
+                                    int c_dtype, int64_t ldc, int *status, const Waits &waits,
+                                    const Launch &L) {
   if (c_dtype == FP4Q_BF16)
-    return launch_o<__nv_bfloat16>(qa, sfa, qb, sfb, M, N, K, c, ldc, status, L);
-  return launch_o<float>(qa, sfa, qb, sfb, M, N, K, c, ldc, status, L);
+    return launch_o<__nv_bfloat16>(qa, sfa, qb, sfb, M, N, K, c, ldc, status, waits, L);
+  return launch_o<float>(qa, sfa, qb, sfb, M, N, K, c, ldc, status, waits, L);
 }
 
 }  // namespace fp4q

@@ -2,6 +2,7 @@
 // extern "C" entry points in api.cu validate arguments and call these.
 #pragma once
 
+#include <climits>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -112,6 +113,17 @@ __device__ __forceinline__ void begin_dependent_tma() {
 }
 #endif
 
+// The bounded waits of the tensor-core kernels.
+constexpr long long kWaitCycles = 2000000000LL;  // ~1 s at the B200's clock
+
+// Those of the MXFP8 kernels as a launch has them: how long a wait may take, and (a
+// failure-detection test hook) after how many K-tiles a CTA's first and second
+// loader, or the loaders of a pair of CTAs, stop issuing.
+struct Waits {
+  long long cycles = kWaitCycles;
+  int stop0 = INT_MAX, stop1 = INT_MAX;
+};
+
 // The host-side argument checks of fp4q_quantize_nvfp4 that need no device
 // (enums, shape, alignment, required pointers); FP4Q_OK or the status that
 // call would return.
@@ -219,7 +231,8 @@ cudaError_t launch_gemm_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8
 // scales per 32 values in the 128x4 tile layout, on the tensor cores
 cudaError_t launch_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const uint8_t *qb,
                                     const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
-                                    int c_dtype, int64_t ldc, int *status, const Launch &L);
+                                    int c_dtype, int64_t ldc, int *status, const Waits &waits,
+                                    const Launch &L);
 
 // A mixture-of-experts layer with MXFP4 weights for a few tokens
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxTopK = 16;

@@ -390,7 +390,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       for (int half = 0; half < 2 && ok; ++half, tile += NT) {
         const uint8_t *fw = sfw + static_cast<int64_t>(tile) * KT * 512;
         for (int kt = k0; kt < k1; ++kt, ++issued) {
-          if (!warp_wait(bars.empty + 8 * ring.s, ring.phase)) {
+          if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, kWaitCycles)) {
             ok = false;
             break;
           }
@@ -415,7 +415,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     }
     if (!ok) {
       *err_ptr = 1;
-      drain_loads<STAGES>(bars.full, issued);
+      drain_loads<STAGES>(bars.full, issued, kWaitCycles);
     }
   } else if (warp == kMma) {
     // the K-tiles with the gate rows, then those with the up rows
@@ -429,14 +429,14 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       const int nb =
           SORTED ? __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[u / NT]) + 15) / 16, 0) : 1;
       const uint32_t idesc = idesc_mx4x8(16 * nb);
-      if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
+      if (!warp_wait(bars.acc_empty + 8 * b, bphase, kWaitCycles)) {
         ok = false;
         break;
       }
       tc_fence_after();
       for (int half = 0; half < 2 && ok; ++half) {
         for (int kt = k0; kt < k1; ++kt) {
-          if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
+          if (!warp_wait(bars.full + 8 * ring.s, ring.phase, kWaitCycles)) {
             ok = false;
             break;
           }
@@ -461,14 +461,14 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       *err_ptr = 1;
       if (elect_one()) tc_commit(bars.drain);
       __syncwarp();
-      warp_wait(bars.drain, 0);
+      warp_wait(bars.drain, 0, kWaitCycles);
     }
   } else {
     const int quarter = warp & 3;
     int i = 0;
     for (int u = cl; u < n_units; u += ncl, ++i) {
       const int b = i & 1, a = u / NT, it = u - a * NT;
-      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1)) {
+      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1, kWaitCycles)) {
         *err_ptr = 1;
         break;
       }
@@ -598,7 +598,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       const uint8_t *fw = sfw + static_cast<int64_t>(wt) * KT * 512;
       const uint8_t *fh = tab.hsf + static_cast<int64_t>(a) * KT * 512;
       for (int kt = k0; kt < k1; ++kt, ++issued) {
-        if (!warp_wait(bars.empty + 8 * ring.s, ring.phase)) {
+        if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, kWaitCycles)) {
           ok = false;
           break;
         }
@@ -623,7 +623,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
     }
     if (!ok) {
       *err_ptr = 1;
-      drain_loads<STAGES>(bars.full, issued);
+      drain_loads<STAGES>(bars.full, issued, kWaitCycles);
     }
   } else if (warp == kMma) {
     Ring<STAGES> ring(0);
@@ -636,13 +636,13 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       const int a = x / KT, k0 = x - a * KT, k1 = min(KT, k0 + hi - x);
       const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[a]) + 15) / 16, 0);
       const uint32_t idesc = idesc_mx4x8(16 * nb);
-      if (!warp_wait(bars.acc_empty + 8 * b, bphase)) {
+      if (!warp_wait(bars.acc_empty + 8 * b, bphase, kWaitCycles)) {
         ok = false;
         break;
       }
       tc_fence_after();
       for (int kt = k0; kt < k1; ++kt) {
-        if (!warp_wait(bars.full + 8 * ring.s, ring.phase)) {
+        if (!warp_wait(bars.full + 8 * ring.s, ring.phase, kWaitCycles)) {
           ok = false;
           break;
         }
@@ -667,14 +667,14 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       *err_ptr = 1;
       if (elect_one()) tc_commit(bars.drain);
       __syncwarp();
-      warp_wait(bars.drain, 0);
+      warp_wait(bars.drain, 0, kWaitCycles);
     }
   } else if (lo < hi) {
     const int quarter = warp & 3, row = quarter * 32 + lane;
     int i = 0;
     for (int a = lo / KT; a <= (hi - 1) / KT; ++a, ++i) {
       const int b = i & 1;
-      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1)) {
+      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1, kWaitCycles)) {
         *err_ptr = 1;
         break;
       }

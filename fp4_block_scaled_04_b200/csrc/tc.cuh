@@ -9,10 +9,9 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "launch.h"
 
 namespace fp4q {
-
-constexpr long long kWaitCycles = 2000000000LL;  // ~1 s at the B200's clock
 
 // Shared-memory matrix descriptor, K-major with 128-byte swizzle: rows of
 // 128 bytes, 8-row groups 1024 bytes apart (SBO), LBO 1 (unused for this
@@ -166,13 +165,13 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// mbar_wait by a converged warp, the same answer in every lane; the clock is
-// read only when the phase has not completed yet.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+// mbar_wait by a converged warp for at most `limit` cycles, the same answer in
+// every lane; the clock is read only when the phase has not completed yet.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long limit) {
   if (__all_sync(0xFFFFFFFFu, mbar_test(bar, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(0xFFFFFFFFu, mbar_test(bar, parity)))
-    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitCycles)) return false;
+    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > limit)) return false;
   return true;
 }
 
@@ -208,12 +207,13 @@ struct Ring {
   }
 };
 
-// After an error: waits (bounded) until the loads of the last `issued` stages
-// have landed, so that none is in flight when the CTA ends.
+// After an error, when no role issues any more: waits (bounded) until the loads of
+// the last of `issued` stages have landed, so that none is in flight when the CTA
+// ends.
 template <int STAGES>
-__device__ __forceinline__ void drain_loads(uint32_t full, int issued) {
+__device__ __forceinline__ void drain_loads(uint32_t full, int issued, long long limit) {
   for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
-    warp_wait(full + 8 * (i % STAGES), (i / STAGES) & 1);
+    warp_wait(full + 8 * (i % STAGES), (i / STAGES) & 1, limit);
 }
 
 // Cluster barrier (every thread of every CTA of the cluster arrives) and
@@ -299,16 +299,31 @@ __device__ __forceinline__ bool mbar_test_cluster(uint32_t bar, uint32_t parity)
       : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
+                                                  long long limit) {
   if (__all_sync(0xFFFFFFFFu, mbar_test_cluster(bar, parity))) return true;
   const long long t0 = clock64();
   while (!__all_sync(0xFFFFFFFFu, mbar_test_cluster(bar, parity)))
-    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > kWaitCycles)) return false;
+    if (__any_sync(0xFFFFFFFFu, clock64() - t0 > limit)) return false;
   return true;
 }
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t peer_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_bar)
                : "memory");
+}
+// takes `bytes` off what a barrier of this CTA still expects, as if a copy had landed
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+// a word of a peer's shared memory
+__device__ __forceinline__ void peer_store(uint32_t addr, uint32_t v) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t peer_load_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 // a load into this CTA's shared memory that completes on the leader's barrier
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x,
@@ -342,6 +357,25 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint32_t leader) {
       "[%0], %1;" ::"r"(bar),
       "h"(static_cast<uint16_t>(3u << leader))
       : "memory");
+}
+// drain_loads for the pair, by a warp of the leader when no role of either CTA issues
+// any more.  A stage's barrier lies with the leader, whose loader expects both CTAs'
+// bytes (2 * bytes) when it issues its own.  The two may have stopped at different
+// stages: where the leader alone has issued, the other's bytes are taken as landed;
+// where the other alone has, the barrier is told to expect them.  Either way the
+// phase completes when what was issued has landed.
+template <int STAGES>
+__device__ __forceinline__ void drain_loads_pair(uint32_t full, int leader, int other,
+                                                 uint32_t bytes, long long limit) {
+  for (int i = min(leader, other); i < max(leader, other); ++i)
+    if (elect_one()) {
+      if (leader > other) mbar_complete_tx(full + 8 * (i % STAGES), bytes);
+      else mbar_expect_tx(full + 8 * (i % STAGES), bytes);
+    }
+  __syncwarp();
+  const int n = max(leader, other);
+  for (int i = n > STAGES ? n - STAGES : 0; i < n; ++i)
+    warp_wait_cluster(full + 8 * (i % STAGES), (i / STAGES) & 1, limit);
 }
 // mma_ktile_mx4x8 for the pair: idesc with M = 256; B's scales are two tiles, and
 // those of its first column lie `skip` columns (32 tokens each) into them

@@ -584,6 +584,21 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4(const uint8_t *qa, const uint8_t *sfa, const u
                                   const uint8_t *sfb, int64_t M, int64_t N, int64_t K, void *c,
                                   int c_dtype, int64_t ldc, int *status, void *stream);
 
+/* ---- TEST-ONLY ENTRY POINT: not part of the supported interface ----------
+ * Failure-detection test hook for fp4q_gemm_mxfp8_mxfp4: the same call with
+ * waits of about 10 ms, in which the loading warp of every CTA (above 64
+ * tokens: of the first and the second CTA of every pair) stops after loads0
+ * (loads0 and loads1) K-tiles of 128 values, so that a wait for the next one
+ * runs out.  The kernel sets *status to 1, writes unspecified values to C,
+ * waits for the copies and MMAs in flight, frees its tensor memory and returns,
+ * and the CUDA context stays usable.  status must be non-NULL, K > 0, loads0 and
+ * loads1 >= 0.  For tests only. */
+fp4q_status fp4q_gemm_mxfp8_mxfp4_withhold_loads(const uint8_t *qa, const uint8_t *sfa,
+                                                 const uint8_t *qb, const uint8_t *sfb, int64_t M,
+                                                 int64_t N, int64_t K, void *c, int c_dtype,
+                                                 int64_t ldc, int64_t loads0, int64_t loads1,
+                                                 int *status, void *stream);
+
 /* A whole mixture-of-experts layer with MXFP4 weights for a few tokens: the
  * routing, both products, the activation and the weighted sum, in two kernels.
  *   p    = softmax of the T x E logits, row by row, in FP32; the top_k largest
