@@ -122,6 +122,9 @@ _SIGNATURES = {
     "fp4q_moe_mxfp4_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "fp4q_moe_mxfp4": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _I64, _I, _P,
                             _I, _I64, _P, _SZ, _P, _P]),
+    "fp4q_moe_mxfp4_withhold_loads": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _I64, _I64, _I64, _I64,
+                                           _I64, _I, _P, _I, _I64, _P, _SZ, _I, _I64, _I64, _P,
+                                           _P]),
 }
 
 

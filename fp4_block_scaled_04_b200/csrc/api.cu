@@ -938,15 +938,14 @@ size_t fp4q_moe_mxfp4_workspace_bytes(int64_t T, int64_t E, int64_t top_k, int64
   return moe_workspace_bytes(T, E, top_k, H, I);
 }
 
-fp4q_status fp4q_moe_mxfp4(const uint8_t *xq, const uint8_t *xsf, const void *logits,
-                           int logits_dtype, const uint8_t *w13, const uint8_t *sf13,
-                           const uint8_t *w2, const uint8_t *sf2, int64_t T, int64_t E,
-                           int64_t top_k, int64_t H, int64_t I, int renormalize, void *out,
-                           int out_dtype, int64_t ldo, void *workspace, size_t ws_bytes,
-                           int *status, void *stream) {
-  DeviceGuard guard;
-  if (!valid_dtype(logits_dtype) || !valid_dtype(out_dtype)) return FP4Q_ERR_INVALID_ARG;
-  if (T < 0 || E < 1 || top_k < 1 || top_k > E || H < 0 || I < 0 || ldo < H)
+}  // extern "C"
+
+namespace fp4q {
+namespace {
+fp4q_status moe_checked(const MoeArgs &m, void *workspace, size_t ws_bytes, void *stream) {
+  const int64_t T = m.T, E = m.E, top_k = m.k, H = m.H, I = m.I;
+  if (!valid_dtype(m.logits_dtype) || !valid_dtype(m.out_dtype)) return FP4Q_ERR_INVALID_ARG;
+  if (T < 0 || E < 1 || top_k < 1 || top_k > E || H < 0 || I < 0 || m.ldo < H)
     return FP4Q_ERR_INVALID_ARG;
   if (T > kMoeMaxTokens || E > kMoeMaxExperts || top_k > kMoeMaxTopK)
     return FP4Q_ERR_UNSUPPORTED_SHAPE;
@@ -955,24 +954,59 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t *xq, const uint8_t *xsf, const void *lo
   constexpr int64_t kMost = int64_t{1} << 30;
   if (H > kMost / E || I > kMost / (2 * E)) return FP4Q_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return FP4Q_OK;
-  if (!xq || !xsf || !logits || !w13 || !sf13 || !w2 || !sf2 || !out) return FP4Q_ERR_INVALID_ARG;
+  if (!m.xq || !m.xsf || !m.logits || !m.w13 || !m.sf13 || !m.w2 || !m.sf2 || !m.out)
+    return FP4Q_ERR_INVALID_ARG;
   if (!workspace || ws_bytes < fp4q_moe_mxfp4_workspace_bytes(T, E, top_k, H, I))
     return FP4Q_ERR_WORKSPACE_TOO_SMALL;
-  if (!aligned16(xq) || !aligned16(xsf) || !aligned16(logits) || !aligned32(w13) ||
-      !aligned16(sf13) || !aligned32(w2) || !aligned16(sf2) || !aligned16(out) ||
-      (ldo * elem_size(out_dtype)) % 16 != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  if (!aligned16(m.xq) || !aligned16(m.xsf) || !aligned16(m.logits) || !aligned32(m.w13) ||
+      !aligned16(m.sf13) || !aligned32(m.w2) || !aligned16(m.sf2) || !aligned16(m.out) ||
+      (m.ldo * elem_size(m.out_dtype)) % 16 != 0 ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FP4Q_ERR_MISALIGNED;
   Launch L;
-  FP4Q_TRY(bind_device(xq, stream, &L));
-  for (const void *p : {static_cast<const void *>(xsf), logits, static_cast<const void *>(w13),
-                        static_cast<const void *>(sf13), static_cast<const void *>(w2),
-                        static_cast<const void *>(sf2), static_cast<const void *>(out),
-                        static_cast<const void *>(workspace)})
+  FP4Q_TRY(bind_device(m.xq, stream, &L));
+  for (const void *p : {static_cast<const void *>(m.xsf), m.logits,
+                        static_cast<const void *>(m.w13), static_cast<const void *>(m.sf13),
+                        static_cast<const void *>(m.w2), static_cast<const void *>(m.sf2),
+                        static_cast<const void *>(m.out), static_cast<const void *>(workspace)})
     FP4Q_TRY(check_dev(p, false));
-  FP4Q_TRY(check_dev(status, true));
-  const MoeArgs m = {xq, xsf, logits, logits_dtype, w13, sf13, w2, sf2, T, E, top_k, H, I,
-                     renormalize != 0, out, out_dtype, ldo, status};
+  FP4Q_TRY(check_dev(m.status, true));
   return cuda_status(launch_moe_mxfp4(m, workspace, L));
+}
+}  // namespace
+}  // namespace fp4q
+
+extern "C" {
+
+fp4q_status fp4q_moe_mxfp4(const uint8_t *xq, const uint8_t *xsf, const void *logits,
+                           int logits_dtype, const uint8_t *w13, const uint8_t *sf13,
+                           const uint8_t *w2, const uint8_t *sf2, int64_t T, int64_t E,
+                           int64_t top_k, int64_t H, int64_t I, int renormalize, void *out,
+                           int out_dtype, int64_t ldo, void *workspace, size_t ws_bytes,
+                           int *status, void *stream) {
+  DeviceGuard guard;
+  return moe_checked({xq, xsf, logits, logits_dtype, w13, sf13, w2, sf2, T, E, top_k, H, I,
+                      renormalize != 0, out, out_dtype, ldo, status, Waits{}, Waits{}},
+                     workspace, ws_bytes, stream);
+}
+
+fp4q_status fp4q_moe_mxfp4_withhold_loads(const uint8_t *xq, const uint8_t *xsf,
+                                          const void *logits, int logits_dtype,
+                                          const uint8_t *w13, const uint8_t *sf13,
+                                          const uint8_t *w2, const uint8_t *sf2, int64_t T,
+                                          int64_t E, int64_t top_k, int64_t H, int64_t I,
+                                          int renormalize, void *out, int out_dtype, int64_t ldo,
+                                          void *workspace, size_t ws_bytes, int product,
+                                          int64_t loads0, int64_t loads1, int *status,
+                                          void *stream) {
+  DeviceGuard guard;
+  if (!status || loads0 < 0 || loads1 < 0 || (product != 1 && product != 2))
+    return FP4Q_ERR_INVALID_ARG;
+  const Waits none, some = withheld(loads0, loads1);
+  return moe_checked({xq, xsf, logits, logits_dtype, w13, sf13, w2, sf2, T, E, top_k, H, I,
+                      renormalize != 0, out, out_dtype, ldo, status, product == 1 ? some : none,
+                      product == 2 ? some : none},
+                     workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

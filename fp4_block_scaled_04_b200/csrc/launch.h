@@ -247,6 +247,7 @@ struct MoeArgs {
   int out_dtype;
   int64_t ldo;
   int *status;
+  Waits waits1, waits2;                            // of the first and the second product
 };
 size_t moe_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t H, int64_t I);
 cudaError_t launch_moe_mxfp4(const MoeArgs &m, void *workspace, const Launch &L);

@@ -85,10 +85,12 @@ using Down = Stages<BN, !DEEP ? 4 : BN == 64 ? 7 : 8, DEEP ? 1 : 2, 2, BN * 512>
 template <int STAGES>
 struct Bars {
   uint32_t full, empty, acc_full, acc_empty, drain, tmem_slot, err_slot;
+  uint32_t issued;                                       // [2] K-tiles that each loader issued
   __device__ explicit Bars(uint32_t at)
       : full(at), empty(at + 8 * STAGES), acc_full(at + 16 * STAGES),
         acc_empty(at + 16 * STAGES + 16), drain(at + 16 * STAGES + 32),
-        tmem_slot(at + 16 * STAGES + 40), err_slot(at + 16 * STAGES + 44) {}
+        tmem_slot(at + 16 * STAGES + 40), err_slot(at + 16 * STAGES + 44),
+        issued(at + 16 * STAGES + 48) {}
   // loaders: what arrives on a stage when it is loaded
   __device__ void init(int loaders) const {
     for (int i = 0; i < STAGES; ++i) {
@@ -103,6 +105,28 @@ struct Bars {
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
 };
+
+// After a wait ran out, by a whole CTA whose roles have all ended: its MMAs and copies
+// come to their end before it does.  The loaders may have stopped at different stages;
+// the arrival that a stage lacks is made here, so that its phase completes when what
+// was issued has landed.
+template <int STAGES>
+__device__ __forceinline__ void end_after_error(const Bars<STAGES> &bars, int warp,
+                                                volatile int *issued, long long limit) {
+  if (warp == kMma) {
+    if (elect_one()) tc_commit(bars.drain);
+    __syncwarp();
+    warp_wait(bars.drain, 0, limit);
+  } else if (warp == kLoadW) {
+    const int a = issued[0], b = issued[1];
+    for (int i = min(a, b); i < max(a, b); ++i)
+      if (elect_one()) mbar_arrive(bars.full + 8 * (i % STAGES));
+    __syncwarp();
+    drain_loads<STAGES>(bars.full, max(a, b), limit);
+  }
+  tc_fence_before();
+  __syncthreads();
+}
 
 __device__ __forceinline__ float load_logit(const void *p, int dtype, int64_t i) {
   return dtype == FP4Q_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i])
@@ -318,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, GateUp<BN>::PER_SM)
 gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
                const __grid_constant__ CUtensorMap map_x, const uint8_t *sfw, const uint8_t *sfx,
                const void *logits, int logits_dtype, int T, int E, int k, bool renormalize, int KT,
-               int NT, int S, Table tab, int *status) {
+               int NT, int S, Table tab, int *status, const Waits waits) {
   using C = GateUp<BN>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -329,6 +353,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
   volatile uint32_t *slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (bars.tmem_slot - raw));
   volatile int *err_ptr = reinterpret_cast<volatile int *>(smem_raw + (bars.err_slot - raw));
+  volatile int *issued_ptr = reinterpret_cast<volatile int *>(smem_raw + (bars.issued - raw));
   float *part = reinterpret_cast<float *>(smem_raw + (base - raw));   // [2][BN][128]
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = S > 1 ? blockIdx.x % S : 0, cl = blockIdx.x / S, ncl = gridDim.x / S;
@@ -378,6 +403,7 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
   if (warp == kLoadW || warp == kLoadX) {
     // one warp loads the weights, the other the tokens, each with its scales
     Ring<STAGES> ring(1);                                 // the first round finds it empty
+    const int stop = warp == kLoadW ? waits.stop0 : waits.stop1;
     int issued = 0;
     bool ok = true;
     for (int u = cl; u < n_units && ok; u += ncl) {
@@ -389,8 +415,8 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       const uint8_t *fx = SORTED ? tab.xsf + static_cast<int64_t>(a) * KT * 512 : sfx;
       for (int half = 0; half < 2 && ok; ++half, tile += NT) {
         const uint8_t *fw = sfw + static_cast<int64_t>(tile) * KT * 512;
-        for (int kt = k0; kt < k1; ++kt, ++issued) {
-          if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, kWaitCycles)) {
+        for (int kt = k0; kt < k1 && issued != stop; ++kt, ++issued) {
+          if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, waits.cycles)) {
             ok = false;
             break;
           }
@@ -413,10 +439,8 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       }
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
-    if (!ok) {
-      *err_ptr = 1;
-      drain_loads<STAGES>(bars.full, issued, kWaitCycles);
-    }
+    if (!ok) *err_ptr = 1;
+    if (lane == 0) issued_ptr[warp == kLoadW ? 0 : 1] = issued;
   } else if (warp == kMma) {
     // the K-tiles with the gate rows, then those with the up rows
     Ring<STAGES> ring(0);
@@ -429,14 +453,14 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       const int nb =
           SORTED ? __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[u / NT]) + 15) / 16, 0) : 1;
       const uint32_t idesc = idesc_mx4x8(16 * nb);
-      if (!warp_wait(bars.acc_empty + 8 * b, bphase, kWaitCycles)) {
+      if (!warp_wait(bars.acc_empty + 8 * b, bphase, waits.cycles)) {
         ok = false;
         break;
       }
       tc_fence_after();
       for (int half = 0; half < 2 && ok; ++half) {
         for (int kt = k0; kt < k1; ++kt) {
-          if (!warp_wait(bars.full + 8 * ring.s, ring.phase, kWaitCycles)) {
+          if (!warp_wait(bars.full + 8 * ring.s, ring.phase, waits.cycles)) {
             ok = false;
             break;
           }
@@ -457,18 +481,13 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       if (b == 0) bphase ^= 1;
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
-    if (!ok) {                                            // wait for the MMAs in flight
-      *err_ptr = 1;
-      if (elect_one()) tc_commit(bars.drain);
-      __syncwarp();
-      warp_wait(bars.drain, 0, kWaitCycles);
-    }
+    if (!ok) *err_ptr = 1;
   } else {
     const int quarter = warp & 3;
     int i = 0;
     for (int u = cl; u < n_units; u += ncl, ++i) {
       const int b = i & 1, a = u / NT, it = u - a * NT;
-      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1, kWaitCycles)) {
+      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1, waits.cycles)) {
         *err_ptr = 1;
         break;
       }
@@ -533,7 +552,10 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
   }
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && status && *err_ptr) atomicExch(status, 1);
+  if (*err_ptr) {
+    if (threadIdx.x == 0 && status) atomicExch(status, 1);
+    end_after_error(bars, warp, issued_ptr, waits.cycles);
+  }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(C::TMEM_COLS)
@@ -544,7 +566,7 @@ template <typename OutT, int BN, bool DEEP>
 __global__ void __launch_bounds__(kThreads, Down<BN, DEEP>::PER_SM)
 down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_h,
             const uint8_t *sfw, Table tab, int T, int E, int k, int KT, int NT, int S, OutT *out,
-            int64_t ldo, int *status) {
+            int64_t ldo, int *status, const Waits waits) {
   using C = Down<BN, DEEP>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -556,6 +578,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
   volatile uint32_t *slot_ptr =
       reinterpret_cast<volatile uint32_t *>(smem_raw + (bars.tmem_slot - raw));
   volatile int *err_ptr = reinterpret_cast<volatile int *>(smem_raw + (bars.err_slot - raw));
+  volatile int *issued_ptr = reinterpret_cast<volatile int *>(smem_raw + (bars.issued - raw));
   float *sum = reinterpret_cast<float *>(smem_raw + (sums - raw));
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int rank = blockIdx.x % S, nt = blockIdx.x / S;
@@ -588,6 +611,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
   if (warp == kLoadW || warp == kLoadX) {
     // one warp loads the weights, the other the rows of h, each with its scales
     Ring<STAGES> ring(1);                                 // the first round finds it empty
+    const int stop = warp == kLoadW ? waits.stop0 : waits.stop1;
     int issued = 0;
     bool ok = true;
     for (int x = lo; x < hi && ok;) {
@@ -597,8 +621,8 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       const int wt = __shfl_sync(0xFFFFFFFFu, ch.expert[a], 0) * NT + nt;   // weight tile
       const uint8_t *fw = sfw + static_cast<int64_t>(wt) * KT * 512;
       const uint8_t *fh = tab.hsf + static_cast<int64_t>(a) * KT * 512;
-      for (int kt = k0; kt < k1; ++kt, ++issued) {
-        if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, kWaitCycles)) {
+      for (int kt = k0; kt < k1 && issued != stop; ++kt, ++issued) {
+        if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
         }
@@ -621,10 +645,8 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       x += k1 - k0;
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
-    if (!ok) {
-      *err_ptr = 1;
-      drain_loads<STAGES>(bars.full, issued, kWaitCycles);
-    }
+    if (!ok) *err_ptr = 1;
+    if (lane == 0) issued_ptr[warp == kLoadW ? 0 : 1] = issued;
   } else if (warp == kMma) {
     Ring<STAGES> ring(0);
     int b = 0;                                            // accumulator and its phase
@@ -636,13 +658,13 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       const int a = x / KT, k0 = x - a * KT, k1 = min(KT, k0 + hi - x);
       const int nb = __shfl_sync(0xFFFFFFFFu, (__popcll(ch.mask[a]) + 15) / 16, 0);
       const uint32_t idesc = idesc_mx4x8(16 * nb);
-      if (!warp_wait(bars.acc_empty + 8 * b, bphase, kWaitCycles)) {
+      if (!warp_wait(bars.acc_empty + 8 * b, bphase, waits.cycles)) {
         ok = false;
         break;
       }
       tc_fence_after();
       for (int kt = k0; kt < k1; ++kt) {
-        if (!warp_wait(bars.full + 8 * ring.s, ring.phase, kWaitCycles)) {
+        if (!warp_wait(bars.full + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
         }
@@ -663,18 +685,13 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       if (b == 0) bphase ^= 1;
       ok = ok && !__any_sync(0xFFFFFFFFu, *err_ptr);
     }
-    if (!ok) {                                            // wait for the MMAs in flight
-      *err_ptr = 1;
-      if (elect_one()) tc_commit(bars.drain);
-      __syncwarp();
-      warp_wait(bars.drain, 0, kWaitCycles);
-    }
+    if (!ok) *err_ptr = 1;
   } else if (lo < hi) {
     const int quarter = warp & 3, row = quarter * 32 + lane;
     int i = 0;
     for (int a = lo / KT; a <= (hi - 1) / KT; ++a, ++i) {
       const int b = i & 1;
-      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1, kWaitCycles)) {
+      if (!warp_wait(bars.acc_full + 8 * b, (i / 2) & 1, waits.cycles)) {
         *err_ptr = 1;
         break;
       }
@@ -706,7 +723,10 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
   cluster_sync();                                         // no CTA leaves while it is read
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && status && *err_ptr) atomicExch(status, 1);
+  if (*err_ptr) {
+    if (threadIdx.x == 0 && status) atomicExch(status, 1);
+    end_after_error(bars, warp, issued_ptr, waits.cycles);
+  }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(C::TMEM_COLS)
@@ -764,7 +784,8 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   while (S < 8 && most * S * 2 <= slots && KT1 >= 2 * S) S *= 2;
   e = launch_dependent(k1, S > 1 ? most * S : most < slots ? most : slots, kThreads,
                        GateUp<BN>::SMEM_BYTES, S, L, w13, x, m.sf13, m.xsf, m.logits,
-                       m.logits_dtype, m.T, m.E, m.k, m.renormalize, KT1, NT1, S, tab, m.status);
+                       m.logits_dtype, m.T, m.E, m.k, m.renormalize, KT1, NT1, S, tab, m.status,
+                       m.waits1);
   if (e != cudaSuccess) return e;
   // second product: the largest cluster that leaves every cluster its place
   const int64_t tiles = m.H / 128;
@@ -773,7 +794,7 @@ cudaError_t launch_t(const MoeArgs &m, const Table &tab, const Launch &L) {
   while (S < 8 && tiles * S * 2 <= slots) S *= 2;
   return launch_dependent(k2, tiles * S, kThreads, Down<BN, DEEP>::SMEM_BYTES, S, L, w2, h, m.sf2,
                           tab, m.T, m.E, m.k, NT1, KT1, S, static_cast<OutT *>(m.out), m.ldo,
-                          m.status);
+                          m.status, m.waits2);
 }
 
 }  // namespace

@@ -629,6 +629,22 @@ fp4q_status fp4q_moe_mxfp4(const uint8_t *xq, const uint8_t *xsf, const void *lo
                            int out_dtype, int64_t ldo, void *workspace, size_t ws_bytes,
                            int *status, void *stream);
 
+/* ---- TEST-ONLY ENTRY POINT: not part of the supported interface ----------
+ * Failure-detection test hook for fp4q_moe_mxfp4, as
+ * fp4q_gemm_mxfp8_mxfp4_withhold_loads is for the product: in the first or
+ * second product (product 1 or 2) the warps that load the weights and the
+ * tokens of every CTA stop after loads0 and loads1 K-tiles of 128 values.  For
+ * tests only. */
+fp4q_status fp4q_moe_mxfp4_withhold_loads(const uint8_t *xq, const uint8_t *xsf,
+                                          const void *logits, int logits_dtype,
+                                          const uint8_t *w13, const uint8_t *sf13,
+                                          const uint8_t *w2, const uint8_t *sf2, int64_t T,
+                                          int64_t E, int64_t top_k, int64_t H, int64_t I,
+                                          int renormalize, void *out, int out_dtype, int64_t ldo,
+                                          void *workspace, size_t ws_bytes, int product,
+                                          int64_t loads0, int64_t loads1, int *status,
+                                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

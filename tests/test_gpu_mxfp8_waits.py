@@ -59,3 +59,44 @@ def test_product(M, N, K, loads, dtype):
         assert torch.equal(got, want)
         assert int(status) == 1 and int(later) == 0
         status.zero_()
+
+
+# the loaders of weights and of tokens stop together, and either one before the other
+LOADERS = [(0, 0), (2, 2), (3, 1), (1, 3), (MANY, 1), (1, MANY), (MANY, 0), (0, MANY)]
+
+
+@pytest.mark.parametrize("product", [1, 2])
+@pytest.mark.parametrize("loads", LOADERS)
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (1, 8, 2, 1024, 4096), (13, 8, 2, 2048, 1024), (16, 64, 8, 1024, 1024),  # routing inside
+    (24, 16, 4, 1024, 1024), (40, 16, 4, 1024, 1024), (64, 32, 8, 1024, 2048)])
+def test_expert_layer(T, E, k, H, I, loads, product):
+    g = torch.Generator(device=DEV).manual_seed(T)
+
+    def w4(rows, cols):
+        o = fq.fp4q_quantize_mxfp4(torch.randn(rows, cols, device=DEV, generator=g) * 0.05,
+                                   scale_layout=fq.SCALE_SWIZZLED)
+        return o["q_row"], o["sf_row"]
+
+    (q13, s13), (q2, s2) = w4(E * 2 * I, H), w4(E * H, I)
+    x = fq.fp4q_quantize_mxfp8(torch.randn(T, H, device=DEV, generator=g),
+                               scale_layout=fq.SCALE_SWIZZLED)
+    logits = torch.randn(T, E, device=DEV, generator=g)
+    args = (x["q"], x["sf"], logits, q13.view(E, 2 * I, H // 2), s13, q2.view(E, H, I // 2), s2)
+    want = fq.fp4q_moe_mxfp4(*args, top_k=k)
+    need = fq.lib().fp4q_moe_mxfp4_workspace_bytes(T, E, k, H, I)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    later = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = torch.empty_like(want)
+    p = [t.data_ptr() for t in args]
+    for _ in range(2):
+        rc = fq.lib().fp4q_moe_mxfp4_withhold_loads(
+            *p[:3], 1, *p[3:], T, E, k, H, I, 1, out.data_ptr(), 0, H, ws.data_ptr(), need,
+            product, *loads, status.data_ptr(), fq._raw_stream(0))
+        assert rc == 0
+        # behind it without a pause, in the same workspace
+        got = fq.fp4q_moe_mxfp4(*args, top_k=k, workspace=ws, status=later)
+        assert torch.equal(got, want)
+        assert int(status) == 1 and int(later) == 0
+        status.zero_()

@@ -24,3 +24,13 @@ def test_withheld_loads_of_the_product(L):
     assert call(loads=(-1, 0)) == ARG and call(loads=(0, -1)) == ARG
     assert call(K=160) == SHAPE and call(ldc=120) == ARG and call(ldc=129) == ALIGN
     assert call(M=0) == OK
+
+
+def test_withheld_loads_of_the_expert_layer(L):
+    def call(T=5, product=1, loads=(0, 0), status=A, n=1 << 30, H=256):
+        return L.fp4q_moe_mxfp4_withhold_loads(A, A, A, 1, A, A, A, A, T, 8, 2, H, 128, 1, A, 0,
+                                               256, A, n, product, *loads, status, None)
+    assert call(product=0) == ARG and call(product=3) == ARG and call(status=None) == ARG
+    assert call(loads=(-1, 0)) == ARG and call(loads=(0, -1)) == ARG
+    assert call(T=65) == SHAPE and call(H=192) == SHAPE and call(n=0) == WS
+    assert call(T=0) == OK
