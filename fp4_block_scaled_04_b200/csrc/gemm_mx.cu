@@ -16,6 +16,8 @@
 //
 // Roles (six warps): one loads (TMA and bulk copies, a ring of stages of 128 values
 // of K), one issues the scale copies and MMAs, four read tensor memory and write C.
+// A stage that no load will fill again is not handed back: an arrival that nobody
+// waits for could come after its CTA has ended.
 // Every wait is bounded; one that runs out sets *status.  With few output tiles a
 // cluster shares a tile, each CTA (or pair) taking a part of K; the partial sums
 // meet in shared memory of the cluster and are added in rank order, so equal calls
@@ -121,7 +123,8 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
     bool ok = true;
     for (int u = cl; u < n_units && ok; u += ncl) {
       const uint8_t *fw = sfw + static_cast<int64_t>(u) * KT * 512;
-      for (int kt = k0; kt < k1 && issued != waits.stop0; ++kt, ++issued) {
+      const int end = k0 + min(k1 - k0, waits.stop0 - issued);
+      for (int kt = k0; kt < end; ++kt, ++issued) {
         if (!warp_wait(empty + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
@@ -145,6 +148,7 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
     int b = 0;                                            // accumulator and its phase
     uint32_t bphase = 1;
     bool ok = true;
+    int left = (n_units - cl + ncl - 1) / ncl * (k1 - k0);   // K-tiles
     const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + T::W_BYTES);
     const uint64_t dsf = desc_sf(base + T::SF_OFF);
     constexpr uint32_t idesc = idesc_mx4x8(BN);
@@ -165,11 +169,12 @@ gemm_mx_kernel(const __grid_constant__ CUtensorMap map_w,
         if (elect_one()) {
           mma_ktile_mx4x8(tmem + b * BN, dw + at, dx + at, dsf + at, dsf + at + 32, sf, sf + 4,
                           idesc, kt != k0);
-          tc_commit(empty + 8 * ring.s);
+          if (left > STAGES) tc_commit(empty + 8 * ring.s);
           if (kt == k1 - 1) tc_commit(acc_full + 8 * b);
         }
         __syncwarp();
         ring.next();
+        --left;
       }
       b ^= 1;
       if (b == 0) bphase ^= 1;
@@ -354,7 +359,8 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
       tile_of(u, plan.nt_m, plan.nt_n, &mt, &nt);
       const int wt = 2 * nt + static_cast<int>(half);     // this CTA's weight tile
       const int m0 = mt * cols, x0 = m0 + static_cast<int>(half) * (cols / 2);
-      for (int kt = k0; kt < k1 && issued != stop; ++kt, ++issued) {
+      const int end = k0 + min(k1 - k0, stop - issued);
+      for (int kt = k0; kt < end; ++kt, ++issued) {
         if (!warp_wait_cluster(empty + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
@@ -382,6 +388,7 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
       int b = 0;                                          // accumulator and its phase
       uint32_t bphase = 1;
       bool ok = true;
+      int left = (n_units - cl + ncl - 1) / ncl * (k1 - k0);   // K-tiles
       const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + T::W_BYTES);
       const uint64_t dsf = desc_sf(base + T::SF_OFF);
       // M = 256: bits 24-28 hold M / 16
@@ -407,11 +414,12 @@ gemm_mx_pair_kernel(const __grid_constant__ CUtensorMap map_w,
           if (elect_one()) {
             mma_ktile_mx4x8_pair(tmem + b * cols, dw + at, dx + at, dsf + at,
                                  tmem + T::SF_AT + T::SF_COLS * ring.s, skip, idesc, kt != k0);
-            tc_commit_pair(empty + 8 * ring.s, leader);
+            if (left > STAGES) tc_commit_pair(empty + 8 * ring.s, leader);
             if (kt == k1 - 1) tc_commit_pair(acc_full + 8 * b, leader);
           }
           __syncwarp();
           ring.next();
+          --left;
         }
         if (++b == nacc) {
           b = 0;

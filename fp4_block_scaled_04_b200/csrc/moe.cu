@@ -415,7 +415,8 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
       const uint8_t *fx = SORTED ? tab.xsf + static_cast<int64_t>(a) * KT * 512 : sfx;
       for (int half = 0; half < 2 && ok; ++half, tile += NT) {
         const uint8_t *fw = sfw + static_cast<int64_t>(tile) * KT * 512;
-        for (int kt = k0; kt < k1 && issued != stop; ++kt, ++issued) {
+        const int end = k0 + min(k1 - k0, stop - issued);
+        for (int kt = k0; kt < end; ++kt, ++issued) {
           if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, waits.cycles)) {
             ok = false;
             break;
@@ -447,6 +448,8 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
     int b = 0;                                            // accumulators and their phase
     uint32_t bphase = 1;
     bool ok = true;
+    // K-tiles; a stage that no load will fill again is not handed back (as in gemm_mx.cu)
+    int left = (n_units - cl + ncl - 1) / ncl * 2 * (k1 - k0);
     const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
     const uint64_t dsf = desc_sf(base + C::SF_OFF);
     for (int u = cl; u < n_units && ok; u += ncl) {
@@ -470,11 +473,12 @@ gate_up_kernel(const __grid_constant__ CUtensorMap map_w,
           if (elect_one()) {
             mma_ktile_mx4x8(tmem + (2 * b + half) * BN, dw + at, dx + at, dsf + at, dsf + at + 32,
                             sf, sf + 4, idesc, kt != k0);
-            tc_commit(bars.empty + 8 * ring.s);
+            if (left > STAGES) tc_commit(bars.empty + 8 * ring.s);
             if (half == 1 && kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
           }
           __syncwarp();
           ring.next();
+          --left;
         }
       }
       b ^= 1;
@@ -621,7 +625,8 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
       const int wt = __shfl_sync(0xFFFFFFFFu, ch.expert[a], 0) * NT + nt;   // weight tile
       const uint8_t *fw = sfw + static_cast<int64_t>(wt) * KT * 512;
       const uint8_t *fh = tab.hsf + static_cast<int64_t>(a) * KT * 512;
-      for (int kt = k0; kt < k1 && issued != stop; ++kt, ++issued) {
+      const int end = k0 + min(k1 - k0, stop - issued);
+      for (int kt = k0; kt < end; ++kt, ++issued) {
         if (!warp_wait(bars.empty + 8 * ring.s, ring.phase, waits.cycles)) {
           ok = false;
           break;
@@ -652,6 +657,7 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
     int b = 0;                                            // accumulator and its phase
     uint32_t bphase = 1;
     bool ok = true;
+    int left = hi - lo;                                   // K-tiles
     const uint64_t dw = desc_sw128(base), dx = desc_sw128(base + C::X_OFF);
     const uint64_t dsf = desc_sf(base + C::SF_OFF);
     for (int x = lo; x < hi && ok;) {
@@ -674,11 +680,12 @@ down_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ C
         if (elect_one()) {
           mma_ktile_mx4x8(tmem + b * BN, dw + at, dx + at, dsf + at, dsf + at + 32, sf, sf + 4,
                           idesc, kt != k0);
-          tc_commit(bars.empty + 8 * ring.s);
+          if (left > STAGES) tc_commit(bars.empty + 8 * ring.s);
           if (kt == k1 - 1) tc_commit(bars.acc_full + 8 * b);
         }
         __syncwarp();
         ring.next();
+        --left;
       }
       x += k1 - k0;
       b ^= 1;
