@@ -178,7 +178,7 @@ def _matrix(x: torch.Tensor, name: str = "x"):
 
 def _stream(device) -> ctypes.c_void_p:
     """The device's current stream (the raw handle: a Stream object costs 2 us more)."""
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    return ctypes.c_void_p(_raw_stream(device.index))
 
 
 def _check(name: str, status: int):
@@ -308,7 +308,13 @@ def _addr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream      # of a device index, as an integer
+def _raw_stream(index: int) -> int:
+    """The current stream of a device, as an integer.  The first call puts torch's
+    function in this one's place: a torch without CUDA lacks it, and the package
+    imports there too."""
+    global _raw_stream
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    return _raw_stream(index)
 
 
 def _mx_scale_bytes(rows: int, cols: int, scale_layout: int) -> int:
