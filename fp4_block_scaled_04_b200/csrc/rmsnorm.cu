@@ -13,6 +13,9 @@
 //
 // Both are bound by HBM: the forward pass moves 7.03 bytes an element with a
 // BF16 residual, the backward pass 8 with d.
+#include <cfloat>
+#include <cmath>
+
 #include "launch.h"
 #include "mxfp8.cuh"
 
@@ -128,14 +131,38 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// 1 / sqrt(v): the hardware's estimate and one Newton step (every thread works a
-// row's out, and the correctly rounded operations took a third of the row's time)
+// 1 / sqrt(v): the hardware's estimate r and one Newton step on the residual 1 - v r^2
+// from both halves of v r, so that only the last addition rounds visibly (every thread
+// works a row's out, and the square root's and the division's correctly rounded
+// operations took a third of the row's time)
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float r = rsqrtf(v);
-  const float e = __fmaf_rn(-__fmul_rn(v, r), r, 1.0f);
+  const float p = __fmul_rn(v, r), q = __fmaf_rn(v, r, -p);
+  const float e = __fmaf_rn(-q, r, __fmaf_rn(-p, r, 1.0f));
   // at 0 and inf (squares that pass FP32) the step would make NaN of inf and 0
   return v > 0.0f && v < INFINITY ? __fmaf_rn(__fmul_rn(0.5f, r), e, r) : r;
 }
+
+// A row's sum over its number of columns, plus a constant, rounded once: 1 / cols as
+// hi + lo, since RN(1 / cols) alone is off by the same part in every row.  hi comes from
+// the host, rounded down, and lo is kept above 0, so that an infinite sum stays one.
+// (With lo from the host too the FP32 backward pass at 8192 x 4096 took 96 us, 90 so:
+// another schedule.)
+inline float inverse_down(int64_t cols) {
+  const double n = static_cast<double>(cols);
+  const float hi = static_cast<float>(1.0 / n);
+  return hi * n > 1.0 ? std::nextafterf(hi, 0.0f) : hi;
+}
+struct Mean {
+  float hi, lo;
+  static __device__ __forceinline__ Mean of(float hi, int cols) {
+    const float left = __fmaf_rn(-hi, static_cast<float>(cols), 1.0f);
+    return {hi, fmaxf(__fmul_rn(left, hi), FLT_MIN)};
+  }
+  __device__ __forceinline__ float operator()(float sum, float plus) const {
+    return __fmaf_rn(sum, hi, __fmaf_rn(sum, lo, plus));
+  }
+};
 
 // max(m, |a|, |b|)
 __device__ __forceinline__ float max_abs3(float m, float a, float b) {
@@ -181,18 +208,18 @@ __device__ __forceinline__ float row_sum(float v, float *slot, int warp) {
 template <typename T, typename TW, int W, int VPT, bool RING, bool FULL>
 __global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
 rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int64_t ld_res,
-               const TW *weight, float eps, int mode, uint8_t *q, uint8_t *sf, int scale_layout,
-               float *rstd_out, T *sum_out, T *y_out, int depth) {
+               const TW *weight, float inv_cols, float eps, int mode, uint8_t *q, uint8_t *sf,
+               int scale_layout, float *rstd_out, T *sum_out, T *y_out, int depth) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
   extern __shared__ __align__(16) uint8_t ring[];        // [depth][x, residual][G] rows
   __shared__ __align__(16) float slot[2][NW];
   begin_dependent();
+  const Mean mean = Mean::of(inv_cols, cols);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
   const int n8 = cols / 8, bpr = cols / 32;
   const int row_bytes = cols * static_cast<int>(sizeof(T)), tensors = res ? 2 : 1;
   const int64_t srows = scale_rows(rows, scale_layout);
   const int64_t scols = scale_cols(bpr, scale_layout);
-  const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(cols));
   // FULL: every thread has all its vectors (cols == 256 W VPT)
   auto mine = [&](int v8) { return FULL || v8 < n8; };
   // a scale byte's offset: the row's part and the column's
@@ -267,7 +294,7 @@ rmsnorm_kernel(const T *x, int64_t rows, int cols, int64_t ld, const T *res, int
       }
     }
     const float total = row_sum<W>(__fadd_rn(ss.x, ss.y), slot[turn], warp);
-    const float rstd = inv_sqrt(__fmaf_rn(total, inv_cols, eps));
+    const float rstd = inv_sqrt(mean(total, eps));
     if (live && rstd_out && wr == 0 && lane == 0) rstd_out[row] = rstd;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -360,8 +387,8 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
     }
     return launch_dependent(kern, grid, NW * 32, smem, 1, L, static_cast<const T *>(x), rows,
                             static_cast<int>(cols), ld, static_cast<const T *>(res), ld_res,
-                            static_cast<const TW *>(weight), eps, mode, q, sf, layout, rstd,
-                            static_cast<T *>(sum), static_cast<T *>(y), depth);
+                            static_cast<const TW *>(weight), inverse_down(cols), eps, mode, q, sf,
+                            layout, rstd, static_cast<T *>(sum), static_cast<T *>(y), depth);
   };
   using std::false_type;
   using std::integral_constant;
@@ -412,11 +439,12 @@ template <typename T, typename TW, int W, int VPT, bool RING>
 __global__ void __launch_bounds__((W < 4 ? 4 : W) * 32, W <= 16 ? 512 / ((W < 4 ? 4 : W) * 32) : 1)
 rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, const TW *weight,
                         const float *rstd, const T *dsum, int64_t ld_dsum, int64_t rows, int cols,
-                        T *dx, float *part, int depth) {
+                        float inv_cols, T *dx, float *part, int depth) {
   constexpr int NW = W < 4 ? 4 : W, G = NW / W;
   extern __shared__ __align__(16) uint8_t ring[];        // [depth][dy, s, dsum][G] rows, [G] dw
   __shared__ __align__(16) float slot[2][NW];
   begin_dependent();
+  const Mean mean = Mean::of(inv_cols, cols);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, wr = warp % W, grp = warp / W;
   const int n8 = cols / 8;
   const int row_bytes = cols * static_cast<int>(sizeof(T)), tensors = dsum ? 3 : 2;
@@ -431,7 +459,6 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, co
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<float4 *>(mine + (h * n8 + v8) * 16) = make_float4(0, 0, 0, 0);
   }
-  const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(cols));
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   auto place = [&](int stage, int t) { return ((stage * tensors + t) * G + grp) * row_bytes; };
   auto fetch = [&](int stage, int64_t row) {
@@ -510,7 +537,7 @@ rmsnorm_backward_kernel(const T *dy, int64_t ld_dy, const T *s, int64_t ld_s, co
         *reinterpret_cast<float4 *>(mine + (n8 + v8) * 16) = a.b;
       }
     }
-    const float c = __fmul_rn(row_sum<W>(__fadd_rn(dot.x, dot.y), slot[turn], warp), inv_cols);
+    const float c = mean(row_sum<W>(__fadd_rn(dot.x, dot.y), slot[turn], warp), 0.0f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v8 = lane + 32 * (wr + W * j);
@@ -593,7 +620,7 @@ cudaError_t launch_bwd_t(const void *dy, int64_t ld_dy, const void *s, int64_t l
   e = launch_dependent(kern, grid, NW * 32, smem, 1, L, static_cast<const T *>(dy), ld_dy,
                        static_cast<const T *>(s), ld_s, static_cast<const TW *>(weight), rstd,
                        static_cast<const T *>(dsum), ld_dsum, rows, static_cast<int>(cols),
-                       static_cast<T *>(dx), part, depth);
+                       inverse_down(cols), static_cast<T *>(dx), part, depth);
   if (e != cudaSuccess) return e;
   return launch_dependent(dweight_kernel, cols / 32, 1024, 0, 1, L,
                           static_cast<const float *>(part), static_cast<int>(grid),
