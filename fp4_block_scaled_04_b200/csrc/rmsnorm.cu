@@ -412,17 +412,23 @@ cudaError_t launch_fwd(const void *x, int64_t rows, int64_t cols, int64_t ld, co
   auto go = [&](auto w) {
     constexpr int W = decltype(w)::value;
     if (n8 <= 32 * W * 3) return run(w, three, true_type{}, false_type{});
-    if (n8 == 32 * W * 4) return run(w, four, true_type{}, true_type{});
-    if (n8 == 32 * W * 5) return run(w, five, true_type{}, true_type{});
-    if (n8 < 32 * W * 4) return run(w, four, true_type{}, false_type{});
-    return run(w, five, true_type{}, false_type{});
+    // 32 warps: four vectors are 32768 columns, the most there are, and too wide for
+    // a ring in FP32
+    if constexpr (W < 32) {
+      if (n8 == 32 * W * 4) return run(w, four, true_type{}, true_type{});
+      if (n8 == 32 * W * 5) return run(w, five, true_type{}, true_type{});
+      if (n8 > 32 * W * 4) return run(w, five, true_type{}, false_type{});
+    } else if constexpr (sizeof(T) == 2) {
+      if (n8 == 32 * W * 4) return run(w, four, true_type{}, true_type{});
+    }
+    return run(w, four, true_type{}, false_type{});
   };
   if (n8 <= 160) return go(one);
   if (n8 <= 320) return go(integral_constant<int, 2>{});
   if (n8 <= 640) return go(four);
   // while two CTAs fit an SM (see ring_depth); one has more warps
   const int64_t pair = 2 * (res ? 2 : 1) * cols * static_cast<int64_t>(sizeof(T));
-  if (n8 <= 1280 && (pair <= kTwoCtas || sizeof(T) == 2)) return go(integral_constant<int, 8>{});
+  if (n8 <= 1280 && pair <= kTwoCtas) return go(integral_constant<int, 8>{});
   if (ring_depth((res ? 2 : 1) * cols * static_cast<int64_t>(sizeof(T)), 0) == 0)
     return run(integral_constant<int, 32>{}, four, false_type{}, false_type{});
   if (n8 <= 2560) return go(integral_constant<int, 16>{});
@@ -653,13 +659,17 @@ cudaError_t launch_bwd(const void *dy, int64_t ld_dy, const void *s, int64_t ld_
   const int64_t row = cols * static_cast<int64_t>(sizeof(T)), group = (dsum ? 3 : 2) * row;
   if (n8 <= 768 && 2 * group + cols * 4 <= kTwoCtas) return go(integral_constant<int, 8>{});
   if (ring_depth(group, cols * 4) == 0) {
-    // (4096 x 8192 FP32: 97 us on 16 warps, 134 on 32, whose 64 registers a thread spill)
-    if (n8 <= 1024) return run(integral_constant<int, 16>{}, two, std::false_type{});
+    // (4096 x 8192 FP32: 97 us on 16 warps, 134 on 32, whose 64 registers a thread spill;
+    // BF16 rows of up to 14080 columns have a ring)
+    if constexpr (sizeof(T) == 4)
+      if (n8 <= 1024) return run(integral_constant<int, 16>{}, two, std::false_type{});
     if (n8 <= 2048) return run(integral_constant<int, 32>{}, two, std::false_type{});
     return run(integral_constant<int, 32>{}, integral_constant<int, 4>{}, std::false_type{});
   }
-  if (n8 <= 1536) return go(integral_constant<int, 16>{});
-  return go(integral_constant<int, 32>{});
+  // (an FP32 row with a ring has at most 11264 columns)
+  if constexpr (sizeof(T) == 2)
+    if (n8 > 1536) return go(integral_constant<int, 32>{});
+  return go(integral_constant<int, 16>{});
 }
 
 }  // namespace
