@@ -12,7 +12,8 @@
 // Up to 64 tokens (gemm_mx_kernel: 128 weight rows x 16 or 64 tokens, two CTAs an
 // SM) the weights' way from HBM bounds it: 6.4 TB/s at 131072 x 8192 and one token.
 // Above (gemm_mx_pair_kernel: pairs of CTAs, 256 weight rows x up to 256 tokens)
-// the tensor core does, or the power limit: 2.9-3.1 PFLOP/s at 8192 tokens.
+// the tensor core does, or the power limit: at 8192 tokens 2.9 PFLOP/s in a burst, 2.4
+// to 2.8 in a loop, where the clocks fall.
 //
 // Roles (six warps): one loads (TMA and bulk copies, a ring of stages of 128 values
 // of K), one issues the scale copies and MMAs, four read tensor memory and write C.
@@ -274,7 +275,8 @@ cudaError_t launch_t(const uint8_t *qx, const uint8_t *sfx, const uint8_t *qw, c
 // and the MMA (M = 256, issued by the leader) reads both halves of the tokens.
 // A CTA alone is bound by shared-memory traffic (96 KB per K-tile of 128 x 256 x
 // 128: 362 us at 8192 x 14336 x 4096, 25.0 at 333 x 4096 x 14336); in pairs it
-// falls by a third, and so does the traffic from L2 (331 and 22.4 us).
+// falls by a third, and so does the traffic from L2 (331 in a burst, 345 to 400 in a loop
+// of calls, and 21.8 us).
 struct Pair {
   static constexpr int STAGES = 6;
   static constexpr int W_BYTES = 128 * 128, W_TX = W_BYTES / 2;

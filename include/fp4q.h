@@ -354,7 +354,8 @@ fp4q_status fp4q_quantize_mxfp6(const void *x, int dtype, int64_t rows, int64_t 
  *   FP4Q_E8M0_RNE        RN(m / 448) to the nearest power of two
  *   FP4Q_E8M0_OCP_FLOOR  2^(floor(log2 m) - 8)
  * Elements v = RN(x * 2^-e), E4M3 round to nearest even with saturation; a
- * block of zeros has e = -127.
+ * block of zeros has e = -127.  A NaN becomes a NaN code and does not enter its
+ * block's maximum; an infinity takes the largest exponent and decodes as itself.
  *   q    [rows, cols] E4M3 codes, 16-byte aligned
  *   sf   biased exponents e + 127 in scale_layout.  Any number of rows and
  *        blocks may be swizzled here: the layout's rows are rounded up to 128
@@ -370,8 +371,9 @@ fp4q_status fp4q_quantize_mxfp8(const void *x, int dtype, int64_t rows, int64_t 
  * producer of the activation in front of a block-scaled product.  Per row of H
  * = cols values, in FP32:
  *   s    = RN_T(x + residual), or x without a residual (T the dtype of x)
- *   rstd = 1 / sqrt(mean(s^2) + eps)          (the mean in the kernel's order; 0
- *          where the sum of squares passes FP32)
+ *   rstd = 1 / sqrt(mean(s^2) + eps)          (the sum in the kernel's order, then one
+ *          rounding of mean + eps and one of the root; 0 where the sum of squares
+ *          passes FP32)
  *   y    = RN(RN(s * rstd) * weight)
  *   q, sf  MXFP8 of y, as fp4q_quantize_mxfp8 (y itself is not rounded first)
  *   x, residual  [rows, cols] of dtype, leading dimensions ld, ld_residual;
@@ -600,7 +602,8 @@ fp4q_status fp4q_gemm_mxfp8_mxfp4_withhold_loads(const uint8_t *qa, const uint8_
                                                  int *status, void *stream);
 
 /* A whole mixture-of-experts layer with MXFP4 weights for a few tokens: the
- * routing, both products, the activation and the weighted sum, in two kernels.
+ * routing, both products, the activation and the weighted sum, in two kernels
+ * (three above 16 tokens).
  *   p    = softmax of the T x E logits, row by row, in FP32; the top_k largest
  *          are chosen (ties: the lowest index) and, with renormalize != 0,
  *          divided by their sum.  -inf masks an expert (NaN counts as -inf);
